@@ -278,8 +278,7 @@ def prepare(case, seed):
         st["workspace"] = torch.zeros(4096, dtype=torch.uint8, device=DEV)
     elif "h_q" in case:
         logits = case["h_q"] * B * (max(ctx) + 64) * 4 if op == "decode_weights" else 0
-        st["workspace"] = torch.zeros(logits + B * case["h_q"] * 64 * (d + 2) * 4 + (1 << 20), dtype=torch.uint8,
-                                      device=DEV)
+        st["workspace"] = torch.zeros(logits + (16 << 20), dtype=torch.uint8, device=DEV)
     return st
 
 
