@@ -333,6 +333,64 @@ int pa_validate_block_tables(const int32_t *block_tables, int max_blocks_per_seq
                              const int32_t *context_lens, int num_seqs, int block_size, int num_blocks);
 int pa_validate_slots(const int64_t *slot_mapping, int num_tokens, int block_size, int num_blocks);
 
+/* ---- 8-bit cache with a scale for each block and KV head ---------------------------
+ * The finest of the scale granularities here: k_scales and v_scales are device fp32
+ * [num_blocks][h_kv] beside the caches, and KV head h's elements of physical block b are worth
+ * code * scales[b][h] ("深度解构…" section 3.2 and section 四 item 1: the pages name KV quantisation
+ * and leave its granularity open).  The write keeps the scales, so nothing has to be known about
+ * the values beforehand, and an outlier costs precision in its own block only.
+ *
+ * pa_reshape_and_cache_block_scales stores rows as pa_reshape_and_cache does.  For every block
+ * that gets rows, and each KV head, with QMAX = 448 (E4M3) or 127 (INT8) and `first` the lowest
+ * offset in the block that this call writes:
+ *   - s = the smallest bf16 number with QMAX * s >= max|x| over the block's new rows (infinities and
+ *     NaN left out);
+ *   - first = 0: the block begins anew, scale = s;
+ *   - first > 0: scale = max(old scale, s).  If it grew, the rows below `first` are requantised,
+ *     code = rne(code * old scale / scale); rows above the new ones stay as they are.
+ * A new row's code = rne(x / scale) to E4M3 (saturating; NaN stays NaN) or to an integer in
+ * [-127, 127] (NaN gives 0); where the scale is 0 every code is 0.  Codes and scales are
+ * bit-exact functions of the inputs.
+ *   slot_mapping   as in pa_reshape_and_cache, and: the tokens of one block stand next to each
+ *                  other, in any order (as pa_alloc_append_n and pa_alloc_append_batch give them).
+ *                  A block whose tokens stand apart gets unspecified codes and scale;
+ *                  pa_validate_block_runs finds that.  Of tokens with the same slot the last counts.
+ *   cache_dtype    PA_CACHE_E4M3 or PA_CACHE_INT8 (bf16 -> PA_ERR_INVALID_ARG)
+ *   k_scales/v_scales device fp32 [num_blocks][h_kv], read and written; the entries of blocks that
+ *                  hold nothing yet need no value
+ * A block copied by pa_copy_blocks needs its scales copied too: pa_copy_block_scales. */
+int pa_reshape_and_cache_block_scales(const void *key, const void *value, int64_t key_stride, int64_t value_stride,
+                                      void *k_cache, void *v_cache, float *k_scales, float *v_scales,
+                                      const int64_t *slot_mapping, int num_tokens, int h_kv, int head_dim, int block_size,
+                                      int num_blocks, int cache_dtype, void *stream);
+
+/* scales[dst][:] = scales[src][:] for every pair (src, dst) and every layer, for K and for V; pairs
+ * as in pa_copy_blocks.  k_scales/v_scales: host arrays of num_layers device pointers. */
+int pa_copy_block_scales(float *const *k_scales, float *const *v_scales, int num_layers, const int64_t *block_pairs,
+                         int num_pairs, int h_kv, int num_blocks, void *stream);
+
+/* Host copy of the slots of one pa_reshape_and_cache_block_scales call: PA_OK, or PA_ERR_INVALID_ARG when
+ * a slot lies outside the pool or a block's tokens do not stand next to each other. */
+int pa_validate_block_runs(const int64_t *slot_mapping, int num_tokens, int block_size, int num_blocks);
+
+/* pa_decode over such a cache.  Same result as pa_decode over the values code * scale: fp32 sums,
+ * probabilities rounded to fp16 (2^-11) for the product with the codes, relative to the largest
+ * probability * V scale, so that blocks with very different scales add up without loss.
+ *   max_context_len  host-known bound of context_lens; it only sizes the grid
+ *   workspace      device, >= pa_decode_block_scales_workspace_size(...) bytes, 16-byte aligned, zero before
+ *                  its first use; every call leaves it ready for the next one, of whatever sizes, here
+ *                  and in pa_decode_scoremod and pa_decode_weights.  Calls sharing a workspace must not
+ *                  overlap on the GPU (captured graphs included).  After a call that recorded
+ *                  PA_DEVERR_TIMEOUT, zero it again.
+ * At most 4096 sequences and 65536 (sequence, KV head) pairs per call, else PA_ERR_UNSUPPORTED. */
+size_t pa_decode_block_scales_workspace_size(int num_seqs, int h_q, int h_kv, int head_dim, int max_context_len);
+
+int pa_decode_block_scales(void *out, const void *q, const void *k_cache, const void *v_cache, const float *k_scales,
+                           const float *v_scales, const int32_t *block_tables, int max_blocks_per_seq,
+                           const int32_t *context_lens, int num_seqs, int max_context_len, int h_q, int h_kv,
+                           int head_dim, int block_size, int num_blocks, float scale, int cache_dtype, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
 /* ---- host block allocator -----------------------------------------------------
  * A global free pool of num_blocks physical blocks with a reference count per
  * block; sequences own block lists ("深度解构…" sections 2.1-2.3;

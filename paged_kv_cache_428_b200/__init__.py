@@ -83,6 +83,12 @@ def _load() -> ctypes.CDLL:
         "pa_prefill_workspace_size": (sz, []),
         "pa_prefill_ws": (i32, [vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, i32, f32, i32, vp, sz,
                                 vp]),
+        "pa_reshape_and_cache_block_scales": (i32, [vp, vp, i64, i64, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp]),
+        "pa_copy_block_scales": (i32, [vp, vp, i32, vp, i32, i32, i32, vp]),
+        "pa_validate_block_runs": (i32, [vp, i32, i32, i32]),
+        "pa_decode_block_scales_workspace_size": (sz, [i32, i32, i32, i32, i32]),
+        "pa_decode_block_scales": (i32, [vp, vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, i32, f32, i32,
+                                         vp, sz, vp]),
         "pa_device_errors": (i32, [ctypes.POINTER(ctypes.c_uint), i32]),
         "pa_validate_block_tables": (i32, [vp, i32, vp, i32, i32, i32]),
         "pa_validate_slots": (i32, [vp, i32, i32, i32]),
@@ -439,6 +445,118 @@ def pa_copy_blocks(k_caches: Sequence[torch.Tensor], v_caches: Sequence[torch.Te
     _check(_lib.pa_copy_blocks(ctypes.cast(kp, ctypes.c_void_p), ctypes.cast(vp, ctypes.c_void_p), L,
                                block_pairs.data_ptr(), block_pairs.shape[0], block_bytes, ref.shape[0],
                                _stream_ptr(stream)), "pa_copy_blocks")
+
+
+# ------------------------------------------------- 8-bit cache with a scale per block and KV head
+def _on_current_device(stream, *tensors) -> int:
+    """The raw stream of a call whose tensors must all live on the current device."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensor on %s, but the current device is cuda:%d" % (t.device, dev))
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
+        raise ValueError("stream of cuda:%d, but the current device is cuda:%d" % (stream.device_index, dev))
+    return _stream_ptr(stream)
+
+
+QUANT_DTYPES = (torch.uint8, torch.float8_e4m3fn, torch.int8)
+
+
+def _need_block_scales(k_cache, v_cache, k_scales, v_scales) -> None:
+    _need(k_cache, "k_cache", QUANT_DTYPES, 4)
+    _need(v_cache, "v_cache", (k_cache.dtype,), 4)
+    _need(k_scales, "k_scales", (torch.float32,), 2)
+    _need(v_scales, "v_scales", (torch.float32,), 2)
+    if v_cache.shape != k_cache.shape or tuple(k_scales.shape) != tuple(k_cache.shape[:2]) or v_scales.shape != k_scales.shape:
+        raise ValueError("shape mismatch between caches and block scales (scales are [num_blocks, h_kv])")
+
+
+def make_block_scales(num_blocks: int, h_kv: int, device="cuda") -> tuple:
+    """(k_scales, v_scales) for a cache of num_blocks blocks, fp32 [num_blocks, h_kv], zero."""
+    return tuple(torch.zeros((num_blocks, h_kv), dtype=torch.float32, device=device) for _ in range(2))
+
+
+def pa_reshape_and_cache_block_scales(key, value, k_cache, v_cache, k_scales, v_scales, slot_mapping,
+                                      stream=None) -> None:
+    """Write bf16 rows [T, h_kv, d] into 8-bit caches with one scale for each (block, KV head); the scales
+    are kept by the call.  The tokens of one block stand next to each other in slot_mapping."""
+    _need_block_scales(k_cache, v_cache, k_scales, v_scales)
+    r = reshape_call_args(key, value, k_cache, v_cache, slot_mapping)
+    _check(_lib.pa_reshape_and_cache_block_scales(
+        *r[:6], k_scales.data_ptr(), v_scales.data_ptr(), *r[6:13],
+        _on_current_device(stream, key, value, k_cache, v_cache, k_scales, v_scales, slot_mapping)),
+        "pa_reshape_and_cache_block_scales")
+
+
+def pa_copy_block_scales(k_scales: Sequence[torch.Tensor], v_scales: Sequence[torch.Tensor], block_pairs: torch.Tensor,
+                         stream=None) -> None:
+    """pa_copy_blocks for the scales: block_pairs int64 [n, 2] (src, dst); every layer's K and V scales."""
+    if len(k_scales) != len(v_scales) or len(k_scales) == 0:
+        raise ValueError("need the same, non-zero number of K and V scale tensors")
+    for t in list(k_scales) + list(v_scales):
+        _need(t, "scales", (torch.float32,), 2)
+        if t.shape != k_scales[0].shape:
+            raise ValueError("all scale tensors must have the same shape")
+    _need(block_pairs, "block_pairs", (torch.int64,), 2)
+    if block_pairs.shape[1] != 2:
+        raise ValueError("block_pairs must be [n, 2]")
+    L = len(k_scales)
+    kp = (ctypes.c_void_p * L)(*[t.data_ptr() for t in k_scales])
+    vp = (ctypes.c_void_p * L)(*[t.data_ptr() for t in v_scales])
+    _check(_lib.pa_copy_block_scales(ctypes.cast(kp, ctypes.c_void_p), ctypes.cast(vp, ctypes.c_void_p), L,
+                                     block_pairs.data_ptr(), block_pairs.shape[0], k_scales[0].shape[1],
+                                     k_scales[0].shape[0],
+                                     _on_current_device(stream, block_pairs, *k_scales, *v_scales)),
+           "pa_copy_block_scales")
+
+
+def pa_validate_block_runs(slot_mapping: torch.Tensor, block_size: int, num_blocks: int) -> int:
+    """Host copy of the slots of a block-scaled write; returns the status code."""
+    sm = slot_mapping.to("cpu", torch.int64).contiguous()
+    return int(_lib.pa_validate_block_runs(sm.data_ptr(), sm.numel(), block_size, num_blocks))
+
+
+def pa_decode_block_scales_workspace_size(num_seqs: int, h_q: int, h_kv: int, head_dim: int, max_context_len: int) -> int:
+    return int(_lib.pa_decode_block_scales_workspace_size(num_seqs, h_q, h_kv, head_dim, max_context_len))
+
+
+def _split_workspace(workspace, size: int, device) -> torch.Tensor:
+    """The caller's workspace, or a new zero-filled one of `size` bytes."""
+    if workspace is None:
+        return torch.zeros(max(size, 16), dtype=torch.uint8, device=device)
+    _need(workspace, "workspace", (torch.uint8,), 1)
+    return workspace
+
+
+def _need_decode(out, q, k_cache, v_cache, block_tables, context_lens, dtypes) -> None:
+    _need(out, "out", (torch.bfloat16,), 3)
+    _need(q, "q", (torch.bfloat16,), 3)
+    _need(k_cache, "k_cache", dtypes, 4)
+    _need(v_cache, "v_cache", (k_cache.dtype,), 4)
+    _need(block_tables, "block_tables", (torch.int32,), 2)
+    _need(context_lens, "context_lens", (torch.int32,), 1)
+    if out.shape != q.shape or k_cache.shape[3] != q.shape[2] or v_cache.shape != k_cache.shape \
+            or block_tables.shape[0] != q.shape[0] or context_lens.shape[0] != q.shape[0]:
+        raise ValueError("shape mismatch between out, q, caches, block_tables and context_lens")
+
+
+def pa_decode_block_scales(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                           max_context_len: int, scale: float = None, workspace: Optional[torch.Tensor] = None,
+                           stream=None) -> torch.Tensor:
+    """pa_decode over an 8-bit cache with one scale for each (block, KV head); returns out."""
+    _need_decode(out, q, k_cache, v_cache, block_tables, context_lens, QUANT_DTYPES)
+    _need_block_scales(k_cache, v_cache, k_scales, v_scales)
+    B, h_q, d = q.shape
+    NB, h_kv, bs, _ = k_cache.shape
+    ws = _split_workspace(workspace, 0 if workspace is not None else pa_decode_block_scales_workspace_size(
+        B, h_q, h_kv, d, max_context_len), q.device)
+    _check(_lib.pa_decode_block_scales(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+        block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, int(max_context_len), h_q, h_kv, d, bs,
+        NB, 1.0 / math.sqrt(d) if scale is None else float(scale), cache_dtype_code(k_cache), ws.data_ptr(), ws.numel(),
+        _on_current_device(stream, out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, ws)),
+        "pa_decode_block_scales")
+    return out
 
 
 def pa_device_errors(clear: bool = True) -> int:

@@ -10,19 +10,21 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
 CSRC = PKG / "csrc"
+OBJ = PKG / "_build"
 LIB = PKG / "libpa.so"
-SOURCES = [CSRC / "pa_lib.cu", CSRC / "host.cpp", CSRC / "allocator.cpp"]
-HEADERS = [ROOT / "include" / "pa.h", CSRC / "common.cuh", CSRC / "cache_ops.cuh", CSRC / "decode.cuh", CSRC / "decode_mma.cuh", CSRC / "decode_balanced.cuh", CSRC / "decode_allheads.cuh", CSRC / "decode_q8.cuh", CSRC / "prefill.cuh", CSRC / "prefill_tc.cuh", CSRC / "tc.cuh"]
+SOURCES = [CSRC / f for f in ("pa_lib.cu", "pa_block_scales.cu", "host.cpp", "allocator.cpp")]
+HEADERS = [ROOT / "include" / "pa.h"] + sorted(CSRC.glob("*.cuh"))
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC",
     "--expt-relaxed-constexpr",
 ]
 
@@ -41,14 +43,28 @@ def stale() -> bool:
     return any(p.stat().st_mtime > t for p in SOURCES + HEADERS)
 
 
+def _object(src: Path, force: bool, extra: list) -> Path:
+    """The object file of one source, compiled if it is older than a file that it was made from."""
+    obj, dep = OBJ / (src.name + ".o"), OBJ / (src.name + ".d")
+    if not force and obj.exists() and dep.exists():
+        names = dep.read_text().replace("\\\n", " ").split(":", 1)[1].split()
+        made_from = [Path(n) for n in names if Path(n).is_relative_to(ROOT)]
+        if all(p.exists() and p.stat().st_mtime <= obj.stat().st_mtime for p in made_from):
+            return obj
+    cmd = [nvcc(), *NVCC_FLAGS, *extra, "-I", str(ROOT / "include"), "-I", str(CSRC), "-MD", "-MF", str(dep), "-c", str(src),
+           "-o", str(obj)]
+    subprocess.run(cmd, check=True)
+    return obj
+
+
 def build(verbose_ptxas: bool = False, force: bool = False) -> Path:
     if not force and not stale():
         return LIB
-    cmd = [nvcc(), *NVCC_FLAGS, "-I", str(ROOT / "include"), "-I", str(CSRC)]
-    if verbose_ptxas:
-        cmd += ["-Xptxas", "-v"]
-    cmd += [str(s) for s in SOURCES] + ["-o", str(LIB)]
-    subprocess.run(cmd, check=True)
+    OBJ.mkdir(exist_ok=True)
+    extra = ["-Xptxas", "-v"] if verbose_ptxas else []
+    with ThreadPoolExecutor(max_workers=len(SOURCES)) as pool:      # one compiler process per source
+        objects = list(pool.map(lambda src: _object(src, force, extra), SOURCES))
+    subprocess.run([nvcc(), *NVCC_FLAGS, "-shared", *map(str, objects), "-o", str(LIB)], check=True)
     return LIB
 
 

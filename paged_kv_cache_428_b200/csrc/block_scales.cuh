@@ -1,0 +1,255 @@
+// block_scales.cuh -- an 8-bit cache with one scale for each (physical block, KV head), for K and for V:
+// the write that keeps the scales, and what the decode of decode_split.cuh needs to know.
+//
+// The scale of a block is the smallest bf16 number s with QMAX s >= max|x| over the block's rows (QMAX = 448
+// for E4M3, 127 for INT8), kept in fp32.  A code is x / s to nearest, ties to even.  With 8 significant
+// bits in x and in s, and at most 7 in a code, x / s and code * s_old / s_new round in fp32 exactly as in
+// any wider type (a quotient of such numbers that is not a tie is further from one than 2^-17 of it):
+// codes are what the definition says, bit for bit.  Against max|x| / QMAX itself the scale is at most 2^-7
+// larger.
+//
+// Bound by: latency for a decode step's rows; the rows' bytes in and codes out for prompts.
+#pragma once
+
+#include "decode_split.cuh"
+
+namespace pa {
+
+struct BlockScaleWriteParams {
+    const __nv_bfloat16 *key;
+    const __nv_bfloat16 *value;
+    int64_t key_stride;            // elements between consecutive tokens
+    int64_t value_stride;
+    uint8_t *k_cache;
+    uint8_t *v_cache;
+    float *k_scales;               // [num_blocks][h_kv]
+    float *v_scales;
+    const int64_t *slot_mapping;
+    int num_tokens;
+    int h_kv;
+    long long num_slots;
+    int chunk;                     // tokens whose runs one CTA looks after, a power of two
+    int heads;                     // KV heads of one CTA
+};
+
+template <int QT>
+__device__ __forceinline__ constexpr float code_max() { return QT == 1 ? 448.f : 127.f; }
+
+// The smallest bf16 value that is not below amax / QMAX (fp32 division: exact enough, see above).
+template <int QT>
+__device__ __forceinline__ float block_scale_of(float amax)
+{
+    return __uint_as_float((__float_as_uint(__fdiv_rn(amax, code_max<QT>())) + 0xffffu) & 0xffff0000u);
+}
+
+template <int QT>
+__device__ __forceinline__ uint32_t encode4(float x0, float x1, float x2, float x3, float s)
+{
+    if (s == 0.f) return 0u;
+    x0 = __fdiv_rn(x0, s);
+    x1 = __fdiv_rn(x1, s);
+    x2 = __fdiv_rn(x2, s);
+    x3 = __fdiv_rn(x3, s);
+    if constexpr (QT == 1) {
+        return (uint32_t)float2_to_e4m3x2(x0, x1) | ((uint32_t)float2_to_e4m3x2(x2, x3) << 16);
+    } else {
+        return ((uint32_t)float_to_s8_sym(x0) & 0xffu) | (((uint32_t)float_to_s8_sym(x1) & 0xffu) << 8) |
+               (((uint32_t)float_to_s8_sym(x2) & 0xffu) << 16) | ((uint32_t)float_to_s8_sym(x3) << 24);
+    }
+}
+
+// Four codes brought from scale `was` to `now`: rne(code * was / now).
+template <int QT>
+__device__ __forceinline__ uint32_t requantise4(uint32_t w, float was, float now)
+{
+    float2 a, b;
+    if constexpr (QT == 1) {
+        a = e4m3x2_to_float2(w & 0xffffu);
+        b = e4m3x2_to_float2(w >> 16);
+    } else {
+        a = make_float2((float)(int8_t)(w & 0xffu), (float)(int8_t)((w >> 8) & 0xffu));
+        b = make_float2((float)(int8_t)((w >> 16) & 0xffu), (float)(int8_t)(w >> 24));
+    }
+    return encode4<QT>(a.x * was, a.y * was, b.x * was, b.y * was, now);
+}
+
+__device__ __forceinline__ float finite_abs(float x)
+{
+    const float a = fabsf(x);
+    return a < INFINITY ? a : 0.f;                     // infinities and NaN take no part in the scale
+}
+
+constexpr int kScaleWriteWarps = 8;
+constexpr int kScaleWriteMaxChunk = 64;
+
+// A run is a maximal stretch of tokens next to each other whose slots lie in one block.  A CTA looks after
+// the runs that begin in its `chunk` tokens, for `heads` KV heads; a warp takes one (run, head, K or V) at a
+// time: which token owns which row (the later one, if two have the same slot), maximum over the rows, the
+// scale, older rows requantised if it grew, the rows.
+template <int D, int BS, int QT>
+__global__ void __launch_bounds__(kScaleWriteWarps * 32) write_block_scales_kernel(const BlockScaleWriteParams p)
+{
+    constexpr unsigned FULL = 0xffffffffu;
+    constexpr int LPR = D / 8, RPI = 32 / LPR;         // lanes per bf16 row, rows of one load
+    constexpr int KEEP = 8;                            // loads kept in registers
+    constexpr int WINDOW = kScaleWriteMaxChunk + BS;   // tokens whose borders are looked at
+    constexpr int WORDS = (WINDOW + 31) / 32;
+    __shared__ uint32_t border[WORDS + 1];             // bit i: token t0 + i does not continue the run of t0 + i - 1
+    __shared__ int run_first[kScaleWriteMaxChunk];
+    __shared__ int num_runs;
+    __shared__ int owner_of[kScaleWriteWarps][BS];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long t0 = (long long)blockIdx.x * p.chunk;
+
+    auto block_of = [&](long long t) -> long long {    // -1: not a token that is written
+        if (t < 0 || t >= p.num_tokens) return -1;
+        const long long slot = __ldg(reinterpret_cast<const long long *>(p.slot_mapping) + t);
+        return slot >= 0 && slot < p.num_slots ? slot / BS : -1;
+    };
+    if (threadIdx.x == 0) num_runs = 0;
+    __syncthreads();
+    const int window = p.chunk + BS;
+    for (int i = threadIdx.x; i < (window + 31) / 32 * 32; i += blockDim.x) {
+        const long long mine = block_of(t0 + i), before = block_of(t0 + i - 1);
+        const bool starts = mine != before;
+        const uint32_t bits = __ballot_sync(FULL, starts);
+        if (lane == 0) border[i >> 5] = bits;
+        if (i < p.chunk && starts && mine >= 0) run_first[atomicAdd(&num_runs, 1)] = i;
+        if (i < p.chunk && blockIdx.y == 0 && t0 + i < p.num_tokens && p.slot_mapping[t0 + i] >= p.num_slots)
+            record_error(PA_DEVERR_BAD_SLOT);
+    }
+    __syncthreads();
+
+    const int h0 = blockIdx.y * p.heads, nh = min(p.heads, p.h_kv - h0);
+    const int items = num_runs * nh * 2;
+    for (int item = warp; item < items; item += kScaleWriteWarps) {
+        const bool is_v = item & 1;
+        const int h = h0 + (item >> 1) % nh, first_tok = run_first[(item >> 1) / nh];
+        // the run's end: the next border, or (slots given twice) further on
+        int end = first_tok + 1;
+        for (;;) {
+            const uint32_t w = border[end >> 5] >> (end & 31);
+            if (w) {
+                end += __ffs(w) - 1;
+                break;
+            }
+            end = (end | 31) + 1;
+            if (end >= window) break;
+        }
+        const long long blk = block_of(t0 + first_tok);
+        if (end >= window) {
+            end = window;
+            while (block_of(t0 + end) == blk) ++end;
+        }
+        int *owner = owner_of[warp];
+        for (int i = lane; i < BS; i += 32) owner[i] = -1;
+        __syncwarp();
+        int lo = BS, hi = -1;
+        for (int i = first_tok + lane; i < end; i += 32) {
+            const int off = (int)(p.slot_mapping[t0 + i] - blk * BS);
+            atomicMax(&owner[off], (int)(t0 + i));
+            lo = min(lo, off);
+            hi = max(hi, off);
+        }
+        lo = __reduce_min_sync(FULL, lo);
+        hi = __reduce_max_sync(FULL, hi);
+        __syncwarp();
+
+        const __nv_bfloat16 *rows = (is_v ? p.value : p.key) + (size_t)h * D;
+        const int64_t stride = is_v ? p.value_stride : p.key_stride;
+        uint8_t *tile = (is_v ? p.v_cache : p.k_cache) + ((size_t)blk * p.h_kv + h) * BS * D;
+        float *scale = (is_v ? p.v_scales : p.k_scales) + (size_t)blk * p.h_kv + h;
+        const float was = lo > 0 ? *scale : 0.f;       // a block written from its first row on has no older rows
+        const int sub = lane / LPR, col = lane % LPR;
+        uint4 v[KEEP];
+        // rows base + sub, base + sub + RPI, ... of the block, 8 elements of each
+        auto load = [&](int base) {
+#pragma unroll
+            for (int k = 0; k < KEEP; ++k) {
+                const int row = base + k * RPI + sub;
+                const int t = row <= hi ? owner[row] : -1;
+                v[k] = t >= 0 ? __ldg(reinterpret_cast<const uint4 *>(rows + t * stride) + col) : make_uint4(0, 0, 0, 0);
+            }
+        };
+        float amax = 0.f;
+        for (int base = lo; base <= hi; base += KEEP * RPI) {
+            load(base);
+#pragma unroll
+            for (int k = 0; k < KEEP; ++k) {
+                const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = bf16x2_to_float2(w[e]);
+                    amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
+                }
+            }
+        }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, off));
+        const float now = fmaxf(was, block_scale_of<QT>(amax));
+        __syncwarp();                                  // every lane has read the old scale
+        if (lo > 0 && now > was) {
+            // the scale grew: the rows before the first new one move to it (16 codes at a time)
+            for (int i = lane; i < lo * (D / 16); i += 32) {
+                uint4 c = reinterpret_cast<uint4 *>(tile)[i];
+                c.x = requantise4<QT>(c.x, was, now);
+                c.y = requantise4<QT>(c.y, was, now);
+                c.z = requantise4<QT>(c.z, was, now);
+                c.w = requantise4<QT>(c.w, was, now);
+                reinterpret_cast<uint4 *>(tile)[i] = c;
+            }
+        }
+        if (lane == 0) *scale = now;
+        const bool kept = hi - lo < KEEP * RPI;        // the rows are still in registers
+        for (int base = lo; base <= hi; base += KEEP * RPI) {
+            if (!kept) load(base);
+#pragma unroll
+            for (int k = 0; k < KEEP; ++k) {
+                const int row = base + k * RPI + sub;
+                if (row <= hi && owner[row] >= 0) {
+                    const float2 a = bf16x2_to_float2(v[k].x), b = bf16x2_to_float2(v[k].y);
+                    const float2 c = bf16x2_to_float2(v[k].z), d = bf16x2_to_float2(v[k].w);
+                    reinterpret_cast<uint2 *>(tile + (size_t)row * D)[col] =
+                        make_uint2(encode4<QT>(a.x, a.y, b.x, b.y, now), encode4<QT>(c.x, c.y, d.x, d.y, now));
+                }
+            }
+        }
+        __syncwarp();                                  // owner free for the next item
+    }
+}
+
+// scales[dst][:] = scales[src][:] for every (src, dst) pair, layer, and K/V.
+constexpr int kScaleCopyMaxLayers = 128;     // of one launch
+
+struct CopyScalesParams {
+    float *k[kScaleCopyMaxLayers];
+    float *v[kScaleCopyMaxLayers];
+    const int64_t *pairs;
+    int h_kv;
+    int num_blocks;
+};
+
+// grid (num_pairs, layers, 2)
+__global__ void __launch_bounds__(32) copy_scales_kernel(const CopyScalesParams p)
+{
+    const long long src = p.pairs[2 * blockIdx.x], dst = p.pairs[2 * blockIdx.x + 1];
+    if (src < 0 || dst < 0 || src >= p.num_blocks || dst >= p.num_blocks) {
+        if (threadIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) record_error(PA_DEVERR_BAD_PAIR);
+        return;
+    }
+    float *s = blockIdx.z ? p.v[blockIdx.y] : p.k[blockIdx.y];
+    for (int h = threadIdx.x; h < p.h_kv; h += 32) s[dst * p.h_kv + h] = s[src * p.h_kv + h];
+}
+
+// The decode: scales per block, no change of the logits.
+struct BlockScalesExt {
+    struct Args {
+        const float *k_scales;     // [num_blocks][h_kv]
+        const float *v_scales;
+    };
+    struct Row {
+        __device__ __forceinline__ Row(const Args &, const SplitParams &, int, int, int, int) {}
+    };
+};
+
+}  // namespace pa
