@@ -65,6 +65,7 @@ extern "C" {
 #define PA_DEVERR_BAD_PAIR  0x4u  /* a copy pair outside the pool was skipped */
 #define PA_DEVERR_TIMEOUT   0x8u  /* a bounded in-kernel wait ran out */
 #define PA_DEVERR_BAD_CHUNK 0x10u /* a prefill chunk longer than its context was skipped */
+#define PA_DEVERR_BAD_LENGTH 0x20u /* a context longer than its row of attention weights */
 
 typedef enum { PA_CACHE_BF16 = 0, PA_CACHE_E4M3 = 1, PA_CACHE_INT8 = 2 } pa_cache_dtype;
 
@@ -390,6 +391,56 @@ int pa_decode_block_scales(void *out, const void *q, const void *k_cache, const 
                            const int32_t *context_lens, int num_seqs, int max_context_len, int h_q, int h_kv,
                            int head_dim, int block_size, int num_blocks, float scale, int cache_dtype, void *workspace,
                            size_t workspace_bytes, void *stream);
+
+/* ---- attention weights, and eviction by them ---------------------------------------
+ * pa_decode that also keeps count of what every cached token has been worth:
+ *   weights[s][k][t] += sum over the query heads h of KV head k of p[s][h][t],  t < context_lens[s]
+ * p the softmax weights of this step (fp32; they sum to h_q / h_kv over t).
+ *   weights        device fp32, row (s, k) at weights + (s * h_kv + k) * weights_stride; a sequence's rows
+ *                  are set to zero when it starts.  Places at or past context_lens[s] are left alone, and so
+ *                  are the rows of a sequence whose result is not finite (a block outside the pool).
+ *   weights_stride >= max_context_len (else PA_ERR_INVALID_ARG)
+ *   max_context_len host-known bound of context_lens.  A longer context is still attended as a whole, but
+ *                  its weights past the bound are not counted; flags PA_DEVERR_BAD_LENGTH.
+ *   cache_dtype    PA_CACHE_BF16 (other types: PA_ERR_UNSUPPORTED)
+ *   workspace      as in pa_decode_block_scales, of pa_decode_weights_workspace_size(...) bytes (the
+ *                  step's logits are kept there between its two launches)
+ * Two calls that add to the same rows must not overlap on the GPU.  No atomics on the weights: results do
+ * not depend on timing. */
+size_t pa_decode_weights_workspace_size(int num_seqs, int h_q, int h_kv, int head_dim, int max_context_len);
+
+int pa_decode_weights(void *out, float *weights, int64_t weights_stride, const void *q, const void *k_cache,
+                      const void *v_cache, const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                      int num_seqs, int max_context_len, int h_q, int h_kv, int head_dim, int block_size, int num_blocks,
+                      float scale, int cache_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bring every sequence down to at most `budget` cached tokens.  For sequence s with n = context_lens[s]
+ * tokens and each KV head (heads choose on their own), m = min(n, budget) tokens stay: the last
+ * min(m, recent), and of the older ones those with the largest weights; of equal weights the earlier
+ * token stays, and weights that are not above 0 (NaN included) rank as 0.  The kept tokens keep their
+ * order; the j-th one's K and V rows are copied to place j of the sequence's new blocks:
+ *   block_tables, context_lens   the sequences as they are (device, as in pa_decode)
+ *   new_block_tables device int32 [num_seqs][new_max_blocks_per_seq]: fresh blocks for m tokens (e.g. of a
+ *                  new sequence, pa_alloc_append_n).  No block of theirs may be in block_tables of this
+ *                  call: rows would be read after they were overwritten.  The old blocks are only read, so
+ *                  they may be shared.
+ *   kept           device int32 [num_seqs][h_kv][budget]: old positions of the kept tokens, ascending;
+ *                  -1 past the m-th
+ *   new_weights    device fp32, rows of new_weights_stride >= budget as in pa_decode_weights: the kept
+ *                  tokens' weights, then zeros up to the row's end (room for the tokens that follow)
+ *   new_context_lens device int32 [num_seqs]: m
+ *   max_context_len host-known bound of context_lens; sizes the launch (weights_stride >= it)
+ *   cache_dtype    any; only rows of head_dim elements are moved.  (Rows of a block-scaled cache cannot
+ *                  move between blocks.)
+ * new_weights and new_context_lens must not overlap weights and context_lens (PA_ERR_INVALID_ARG).  A context
+ * longer than weights_stride keeps nothing and flags PA_DEVERR_BAD_LENGTH; a row whose block is outside the
+ * pool is skipped and flags PA_DEVERR_BAD_BLOCK.  Tokens keep what positions were worked into their K;
+ * calls that go by distance (windows, distance biases) see the new places. */
+int pa_evict(void *k_cache, void *v_cache, const float *weights, int64_t weights_stride, const int32_t *block_tables,
+             int max_blocks_per_seq, const int32_t *context_lens, const int32_t *new_block_tables, int new_max_blocks_per_seq,
+             int num_seqs, int max_context_len, int budget, int recent, int h_kv, int head_dim, int block_size,
+             int num_blocks, int cache_dtype, int32_t *kept, float *new_weights, int64_t new_weights_stride,
+             int32_t *new_context_lens, void *stream);
 
 /* ---- host block allocator -----------------------------------------------------
  * A global free pool of num_blocks physical blocks with a reference count per

@@ -37,6 +37,7 @@ PA_DEVERR_BAD_BLOCK = 0x2
 PA_DEVERR_BAD_PAIR = 0x4
 PA_DEVERR_TIMEOUT = 0x8
 PA_DEVERR_BAD_CHUNK = 0x10
+PA_DEVERR_BAD_LENGTH = 0x20
 
 STATUS = {0: "PA_OK", -1: "PA_ERR_INVALID_ARG", -2: "PA_ERR_UNSUPPORTED", -3: "PA_ERR_WORKSPACE",
           -4: "PA_ERR_OOM", -5: "PA_ERR_CUDA", -6: "PA_ERR_NOT_FOUND"}
@@ -89,6 +90,11 @@ def _load() -> ctypes.CDLL:
         "pa_decode_block_scales_workspace_size": (sz, [i32, i32, i32, i32, i32]),
         "pa_decode_block_scales": (i32, [vp, vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, i32, f32, i32,
                                          vp, sz, vp]),
+        "pa_decode_weights_workspace_size": (sz, [i32, i32, i32, i32, i32]),
+        "pa_decode_weights": (i32, [vp, vp, i64, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, i32, f32, i32, vp, sz,
+                                    vp]),
+        "pa_evict": (i32, [vp, vp, vp, i64, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, i32, i32, vp, vp, i64, vp,
+                           vp]),
         "pa_device_errors": (i32, [ctypes.POINTER(ctypes.c_uint), i32]),
         "pa_validate_block_tables": (i32, [vp, i32, vp, i32, i32, i32]),
         "pa_validate_slots": (i32, [vp, i32, i32, i32]),
@@ -557,6 +563,61 @@ def pa_decode_block_scales(out, q, k_cache, v_cache, k_scales, v_scales, block_t
         _on_current_device(stream, out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, ws)),
         "pa_decode_block_scales")
     return out
+
+
+# ----------------------------------------------------------- attention weights and eviction by them
+def pa_decode_weights_workspace_size(num_seqs: int, h_q: int, h_kv: int, head_dim: int, max_context_len: int) -> int:
+    return int(_lib.pa_decode_weights_workspace_size(num_seqs, h_q, h_kv, head_dim, max_context_len))
+
+
+def pa_decode_weights(out, weights, q, k_cache, v_cache, block_tables, context_lens, max_context_len: int,
+                      scale: float = None, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """pa_decode that also adds each cached token's softmax weights, summed over the query heads of its KV head,
+    to weights fp32 [B, h_kv, >= max_context_len]; returns out."""
+    _need_decode(out, q, k_cache, v_cache, block_tables, context_lens, CACHE_DTYPES)
+    _need(weights, "weights", (torch.float32,), 3)
+    B, h_q, d = q.shape
+    NB, h_kv, bs, _ = k_cache.shape
+    if weights.shape[0] != B or weights.shape[1] != h_kv:
+        raise ValueError("weights must be [%d, %d, n], got %s" % (B, h_kv, tuple(weights.shape)))
+    ws = _split_workspace(workspace, 0 if workspace is not None else pa_decode_weights_workspace_size(
+        B, h_q, h_kv, d, max_context_len), q.device)
+    _check(_lib.pa_decode_weights(
+        out.data_ptr(), weights.data_ptr(), weights.shape[2], q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, int(max_context_len), h_q, h_kv, d, bs,
+        NB, 1.0 / math.sqrt(d) if scale is None else float(scale), cache_dtype_code(k_cache), ws.data_ptr(), ws.numel(),
+        _on_current_device(stream, out, weights, q, k_cache, v_cache, block_tables, context_lens, ws)),
+        "pa_decode_weights")
+    return out
+
+
+def pa_evict(k_cache, v_cache, weights, block_tables, context_lens, new_block_tables, max_context_len: int, budget: int,
+             recent: int, kept, new_weights, new_context_lens, stream=None) -> None:
+    """Keep at most `budget` tokens of every sequence: the last `recent` and the heaviest of the others, chosen
+    per KV head, their rows copied in order to the blocks of new_block_tables.  Fills kept int32 [B, h_kv, budget],
+    new_weights fp32 [B, h_kv, >= budget] and new_context_lens int32 [B]."""
+    _need(k_cache, "k_cache", CACHE_DTYPES, 4)
+    _need(v_cache, "v_cache", (k_cache.dtype,), 4)
+    _need(weights, "weights", (torch.float32,), 3)
+    _need(new_weights, "new_weights", (torch.float32,), 3)
+    _need(kept, "kept", (torch.int32,), 3)
+    _need(block_tables, "block_tables", (torch.int32,), 2)
+    _need(new_block_tables, "new_block_tables", (torch.int32,), 2)
+    _need(context_lens, "context_lens", (torch.int32,), 1)
+    _need(new_context_lens, "new_context_lens", (torch.int32,), 1)
+    NB, h_kv, bs, d = k_cache.shape
+    B = context_lens.shape[0]
+    if v_cache.shape != k_cache.shape or block_tables.shape[0] != B or new_block_tables.shape[0] != B \
+            or new_context_lens.shape[0] != B or tuple(kept.shape) != (B, h_kv, budget) \
+            or tuple(weights.shape[:2]) != (B, h_kv) or tuple(new_weights.shape[:2]) != (B, h_kv):
+        raise ValueError("shape mismatch between caches, tables, lengths, weights and kept")
+    _check(_lib.pa_evict(
+        k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), weights.shape[2], block_tables.data_ptr(),
+        block_tables.shape[1], context_lens.data_ptr(), new_block_tables.data_ptr(), new_block_tables.shape[1], B,
+        int(max_context_len), int(budget), int(recent), h_kv, d, bs, NB, cache_dtype_code(k_cache), kept.data_ptr(),
+        new_weights.data_ptr(), new_weights.shape[2], new_context_lens.data_ptr(),
+        _on_current_device(stream, k_cache, v_cache, weights, block_tables, context_lens, new_block_tables, kept, new_weights,
+                           new_context_lens)), "pa_evict")
 
 
 def pa_device_errors(clear: bool = True) -> int:

@@ -247,6 +247,7 @@ struct BlockScalesExt {
         const float *k_scales;     // [num_blocks][h_kv]
         const float *v_scales;
     };
+    template <int G>
     struct Row {
         __device__ __forceinline__ Row(const Args &, const SplitParams &, int, int, int, int) {}
     };

@@ -260,8 +260,8 @@ __device__ __forceinline__ SplitPlace split_locate(const int *prefix, int num_se
     return at;
 }
 
-// Ext: struct with `Args` (kernel argument), `Row` (bf16 only: built per group, see split_consume_bf16) and,
-// for codes, k_scales / v_scales [num_blocks][h_kv] in Args.
+// Ext: struct with `Args` (kernel argument), `Row<G>` (built per group; its functions for bf16 only, see
+// split_consume_bf16) and, for codes, k_scales / v_scales [num_blocks][h_kv] in Args.
 template <int D, int BS, int G, int QT, class Ext>
 __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, 5)
     paged_decode_split_kernel(const SplitParams p, const typename Ext::Args args,
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, 5)
         }
         SplitState<MT> state;
         state.clear();
-        const typename Ext::Row row(args, p, at.seq, at.kvh, ctx, lane);
+        const typename Ext::template Row<G> row(args, p, at.seq, at.kvh, ctx, lane);
         bool bad = false;
         for (int i = (warp - k0) & (NW - 1); i < n; i += NW) {
             if (*abort_flag) break;

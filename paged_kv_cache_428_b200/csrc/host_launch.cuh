@@ -218,5 +218,6 @@ int collect_device_errors(unsigned int *flags, int clear)
 }  // namespace
 
 int block_scales_errors(unsigned int *flags, int clear);    // pa_block_scales.cu
+int evict_errors(unsigned int *flags, int clear);           // pa_evict.cu
 
 }  // namespace pa

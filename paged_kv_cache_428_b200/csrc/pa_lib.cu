@@ -1000,6 +1000,7 @@ int pa_device_errors(unsigned int *flags, int clear)
     unsigned int v = 0;
     int rc = collect_device_errors(&v, clear);
     if (rc == PA_OK) rc = block_scales_errors(&v, clear);
+    if (rc == PA_OK) rc = evict_errors(&v, clear);
     if (rc != PA_OK) return rc;
     *flags = v;
     return PA_OK;
