@@ -334,6 +334,44 @@ int pa_validate_block_tables(const int32_t *block_tables, int max_blocks_per_seq
                              const int32_t *context_lens, int num_seqs, int block_size, int num_blocks);
 int pa_validate_slots(const int64_t *slot_mapping, int num_tokens, int block_size, int num_blocks);
 
+/* ---- attention with modified scores -------------------------------------------------
+ * Decode and chunked prefill ("现代 AI…" section 1, attention formula) with what many models do to the
+ * scores before the softmax.  With p the position of the query row (context_lens[s] - 1 for a decode
+ * step) and t that of the key, in this order:
+ *   x = scale * q . k
+ *   softcap > 0:    x = softcap * tanh(x / softcap)      (0 = no cap; negative or not finite:
+ *                   PA_ERR_INVALID_ARG)
+ *   alibi_slopes:   x = x - alibi_slopes[h] * |p - t|    (device fp32 [h_q], finite; NULL = no bias)
+ *   window > 0:     only tokens t > p - window are seen, the query's own among them (0 = no window)
+ *   prefix_lens:    tokens t < prefix_lens[s] are seen by every row of sequence s (inside its window),
+ *                   also those behind it (device int32 [num_seqs], at most context_lens[s] count; NULL =
+ *                   causal).  Prefill only: a decode step sees no token behind it.
+ * and out = softmax(x) . V over the tokens seen.  Documents that must not see each other are sequences of
+ * their own here (a row of block_tables and a stretch of query_start each), which is what a document mask
+ * says.
+ * Blocks that lie before the window of every row of the call are not read: their table entries need not be
+ * valid, so that a serving program can give them away.  bf16 caches (others: PA_ERR_UNSUPPORTED).
+ * Accuracy as pa_decode and pa_prefill; tanh to an absolute 2^-22 of the cap.
+ *
+ * pa_decode_scoremod: arguments as pa_decode.  workspace as in pa_decode_block_scales, of
+ * pa_decode_scoremod_workspace_size(...) bytes; the same limits. */
+size_t pa_decode_scoremod_workspace_size(int num_seqs, int h_q, int h_kv, int head_dim, int max_context_len, int window);
+
+int pa_decode_scoremod(void *out, const void *q, const void *k_cache, const void *v_cache, const int32_t *block_tables,
+                       int max_blocks_per_seq, const int32_t *context_lens, int num_seqs, int max_context_len, int h_q,
+                       int h_kv, int head_dim, int block_size, int num_blocks, float scale, float softcap,
+                       const float *alibi_slopes, int window, int cache_dtype, void *workspace, size_t workspace_bytes,
+                       void *stream);
+
+/* pa_prefill_scoremod: arguments, workspace (pa_prefill_workspace_size bytes) and errors as pa_prefill_ws, but
+ * scale may have any sign.  Rows of one chunk are worked on in tiles: V of tokens that some rows of a tile see
+ * and others do not must be finite (as in pa_prefill). */
+int pa_prefill_scoremod(void *out, const void *q, const void *k_cache, const void *v_cache, const int32_t *block_tables,
+                        int max_blocks_per_seq, const int32_t *query_start, const int32_t *context_lens, int num_seqs,
+                        int max_query_len, int h_q, int h_kv, int head_dim, int block_size, int num_blocks, float scale,
+                        float softcap, const float *alibi_slopes, int window, const int32_t *prefix_lens, int cache_dtype,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
 /* ---- 8-bit cache with a scale for each block and KV head ---------------------------
  * The finest of the scale granularities here: k_scales and v_scales are device fp32
  * [num_blocks][h_kv] beside the caches, and KV head h's elements of physical block b are worth

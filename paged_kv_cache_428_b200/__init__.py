@@ -84,6 +84,11 @@ def _load() -> ctypes.CDLL:
         "pa_prefill_workspace_size": (sz, []),
         "pa_prefill_ws": (i32, [vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, i32, f32, i32, vp, sz,
                                 vp]),
+        "pa_decode_scoremod_workspace_size": (sz, [i32, i32, i32, i32, i32, i32]),
+        "pa_decode_scoremod": (i32, [vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, i32, f32, f32, vp, i32, i32, vp,
+                                     sz, vp]),
+        "pa_prefill_scoremod": (i32, [vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, i32, f32, f32, vp, i32, vp,
+                                      i32, vp, sz, vp]),
         "pa_reshape_and_cache_block_scales": (i32, [vp, vp, i64, i64, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp]),
         "pa_copy_block_scales": (i32, [vp, vp, i32, vp, i32, i32, i32, vp]),
         "pa_validate_block_runs": (i32, [vp, i32, i32, i32]),
@@ -562,6 +567,61 @@ def pa_decode_block_scales(out, q, k_cache, v_cache, k_scales, v_scales, block_t
         NB, 1.0 / math.sqrt(d) if scale is None else float(scale), cache_dtype_code(k_cache), ws.data_ptr(), ws.numel(),
         _on_current_device(stream, out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, ws)),
         "pa_decode_block_scales")
+    return out
+
+
+# ------------------------------------------------------------------- attention with modified scores
+def pa_decode_scoremod_workspace_size(num_seqs: int, h_q: int, h_kv: int, head_dim: int, max_context_len: int,
+                                      window: int = 0) -> int:
+    return int(_lib.pa_decode_scoremod_workspace_size(num_seqs, h_q, h_kv, head_dim, max_context_len, window))
+
+
+def _slopes_ptr(alibi_slopes, h_q: int) -> Optional[int]:
+    if alibi_slopes is None:
+        return None
+    _need(alibi_slopes, "alibi_slopes", (torch.float32,), 1)
+    if alibi_slopes.shape[0] != h_q:
+        raise ValueError("alibi_slopes: expected %d, got %d" % (h_q, alibi_slopes.shape[0]))
+    return alibi_slopes.data_ptr()
+
+
+def pa_decode_scoremod(out, q, k_cache, v_cache, block_tables, context_lens, max_context_len: int, softcap: float = 0.0,
+                       alibi_slopes: Optional[torch.Tensor] = None, window: int = 0, scale: float = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """pa_decode with scores capped by softcap * tanh(x / softcap), less alibi_slopes[h] times the distance, over
+    the last `window` tokens; each is off by default.  Returns out."""
+    _need_decode(out, q, k_cache, v_cache, block_tables, context_lens, CACHE_DTYPES)
+    B, h_q, d = q.shape
+    NB, h_kv, bs, _ = k_cache.shape
+    ws = _split_workspace(workspace, 0 if workspace is not None else pa_decode_scoremod_workspace_size(
+        B, h_q, h_kv, d, max_context_len, window), q.device)
+    _check(_lib.pa_decode_scoremod(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+        block_tables.shape[1], context_lens.data_ptr(), B, int(max_context_len), h_q, h_kv, d, bs, NB,
+        1.0 / math.sqrt(d) if scale is None else float(scale), float(softcap), _slopes_ptr(alibi_slopes, h_q), int(window),
+        cache_dtype_code(k_cache), ws.data_ptr(), ws.numel(),
+        _on_current_device(stream, out, q, k_cache, v_cache, block_tables, context_lens, alibi_slopes, ws)),
+        "pa_decode_scoremod")
+    return out
+
+
+def pa_prefill_scoremod(out, q, k_cache, v_cache, block_tables, query_start, context_lens, max_query_len: int,
+                        workspace: torch.Tensor, softcap: float = 0.0, alibi_slopes: Optional[torch.Tensor] = None,
+                        window: int = 0, prefix_lens: Optional[torch.Tensor] = None, scale: float = None,
+                        stream=None) -> torch.Tensor:
+    """pa_prefill_ws with modified scores (see pa_decode_scoremod); tokens before prefix_lens[s] (int32 [B]) are
+    seen by all rows of sequence s.  workspace: make_prefill_workspace().  Returns out."""
+    a = prefill_call_args(out, q, k_cache, v_cache, block_tables, query_start, context_lens, max_query_len, scale)
+    _need(workspace, "workspace", (torch.uint8,), 1)
+    if prefix_lens is not None:
+        _need(prefix_lens, "prefix_lens", (torch.int32,), 1)
+        if prefix_lens.shape[0] != context_lens.shape[0]:
+            raise ValueError("prefix_lens: expected %d, got %d" % (context_lens.shape[0], prefix_lens.shape[0]))
+    _check(_lib.pa_prefill_scoremod(
+        *a[:16], float(softcap), _slopes_ptr(alibi_slopes, q.shape[1]), int(window),
+        None if prefix_lens is None else prefix_lens.data_ptr(), a[16], workspace.data_ptr(), workspace.numel(),
+        _on_current_device(stream, out, q, k_cache, v_cache, block_tables, query_start, context_lens, alibi_slopes,
+                           prefix_lens, workspace)), "pa_prefill_scoremod")
     return out
 
 

@@ -219,5 +219,6 @@ int collect_device_errors(unsigned int *flags, int clear)
 
 int block_scales_errors(unsigned int *flags, int clear);    // pa_block_scales.cu
 int evict_errors(unsigned int *flags, int clear);           // pa_evict.cu
+int scoremod_errors(unsigned int *flags, int clear);        // pa_scoremod.cu
 
 }  // namespace pa

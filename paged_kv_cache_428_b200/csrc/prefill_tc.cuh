@@ -53,6 +53,9 @@
 //              the start of an item it loads the item's whole query tiles (3-D TMA of q, one box
 //              per tile) once both tiles have released the previous item's last K tile, i.e. once
 //              every S product that read the Q tiles has finished.
+// Modified scores.  `Mod` changes what a score becomes and which tokens a row sees; every difference
+// stands under `if constexpr (Mod::kOn)`, and PrefillPlain is the kernel without any (see
+// scoremod_prefill.cuh for the other one).
 // Every wait on the data path is bounded and also ends when another role has stopped the CTA; on
 // a timeout or a bad block the CTA records the error, stops claiming, writes NaN into the rows
 // of the items it holds, waits for its copies and MMAs in flight and frees its tensor memory.
@@ -166,6 +169,11 @@ struct PrefillSched {
     int q_tma;          // the Q tensor map is valid: query tiles inside their chunk come by TMA
 };
 
+// No modification: causal softmax of the scaled scores.
+struct PrefillPlain {
+    static constexpr bool kOn = false;
+};
+
 template <int D, int BS, int G, int NQ_ = 2, int KST_ = 4, int VST_ = 4>
 struct PrefillTcConfig {
     static constexpr int NQ = NQ_;                        // 128-row query tiles per item
@@ -212,13 +220,15 @@ struct PrefillTcConfig {
 };
 
 // Item layout in the ring: seq (< 0: no more items), KV head, pair, first query row, chunk
-// length, context length, KV tiles of query tile 0 and of query tile 1.
+// length, context length, KV tiles of query tile 0 and of query tile 1 (with a window, counted from the
+// first KV tile that the pair's first row sees).
 enum { IT_SEQ, IT_KVH, IT_PAIR, IT_Q0, IT_CHUNK, IT_CTX, IT_NKV0, IT_NKV1, IT_N };
 
-template <int D, int BS, int G, int NQ_ = 2, int KST_ = 4, int VST_ = 4>
+template <int D, int BS, int G, class Mod = PrefillPlain, int NQ_ = 2, int KST_ = 4, int VST_ = 4>
 __global__ void __launch_bounds__(PrefillTcConfig<D, BS, G, NQ_, KST_, VST_>::THREADS, 1)
     paged_prefill_tc_kernel(const PrefillParams p, const PrefillSched sc, const __grid_constant__ CUtensorMap tmap_k,
-                            const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_q)
+                            const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_q,
+                            const Mod mod)
 {
     using C = PrefillTcConfig<D, BS, G, NQ_, KST_, VST_>;
     constexpr int KST = C::KST, VST = C::VST, BN = C::BN, NQ = C::NQ;
@@ -318,9 +328,20 @@ __global__ void __launch_bounds__(PrefillTcConfig<D, BS, G, NQ_, KST_, VST_>::TH
     };
     // query tile q of a pair lies wholly inside the chunk: its Q tile comes by one TMA load
     auto q_by_tma = [&](int pair, int chunk, int q) { return sc.q_tma && (pair * NQ + q + 1) * C::TQ <= chunk; };
-    auto nkv_tile = [&](int chunk, int ctx, int pair, int q) {
+    // first token that any row of a pair sees (the window of its first row), and the KV tiles of its
+    // query tile q, counted from the tile that holds it
+    auto first_token = [&](int chunk, int ctx, int pair) {
+        if constexpr (Mod::kOn) return mod.first_token(ctx - chunk + pair * NQ * C::TQ);
+        else return 0;
+    };
+    auto nkv_tile = [&](int seq, int chunk, int ctx, int pair, int q) {
         const int t0 = (pair * NQ + q) * C::TQ;
-        return t0 >= chunk ? 0 : ceil_div(ctx - chunk + min(chunk, t0 + C::TQ), BN);
+        if constexpr (Mod::kOn) {
+            const int end = max(ctx - chunk + min(chunk, t0 + C::TQ), min(ctx, mod.prefix(seq)));
+            return t0 >= chunk ? 0 : ceil_div(end, BN) - first_token(chunk, ctx, pair) / BN;
+        } else {
+            return t0 >= chunk ? 0 : ceil_div(ctx - chunk + min(chunk, t0 + C::TQ), BN);
+        }
     };
 
 
@@ -391,8 +412,8 @@ __global__ void __launch_bounds__(PrefillTcConfig<D, BS, G, NQ_, KST_, VST_>::TH
                     it[IT_Q0] = q0;
                     it[IT_CHUNK] = chunk;
                     it[IT_CTX] = ctx;
-                    it[IT_NKV0] = nkv_tile(chunk, ctx, pair, 0);
-                    it[IT_NKV1] = NQ > 1 ? nkv_tile(chunk, ctx, pair, 1) : 0;
+                    it[IT_NKV0] = nkv_tile(seq, chunk, ctx, pair, 0);
+                    it[IT_NKV1] = NQ > 1 ? nkv_tile(seq, chunk, ctx, pair, 1) : 0;
                     break;
                 }
             }
@@ -459,13 +480,14 @@ __global__ void __launch_bounds__(PrefillTcConfig<D, BS, G, NQ_, KST_, VST_>::TH
             auto entry = [&](int lb) -> int {
                 return (lb < nblk_seq && lb < p.max_blocks_per_seq) ? __ldg(trow + lb) : -1;
             };
-            int ecur = entry(lane), enxt = entry(32 + lane);
+            const int tok_lo = first_token(cur[IT_CHUNK], ctx, cur[IT_PAIR]), t_lo = tok_lo / BN;
+            int ecur = entry(t_lo * BPT + lane), enxt = entry(t_lo * BPT + 32 + lane);
             const int row_kvh = cur[IT_KVH];
             bool next_known = is_v;                            // K warp: next item claimed and published
             for (int t = 0; t < nkv; ++t) {
                 if (t > 0 && t % TPB == 0) {
                     ecur = enxt;
-                    enxt = entry((t / TPB + 1) * 32 + lane);
+                    enxt = entry(t_lo * BPT + (t / TPB + 1) * 32 + lane);
                 }
                 const int st = issued % nst;
                 int go = 1;
@@ -477,9 +499,13 @@ __global__ void __launch_bounds__(PrefillTcConfig<D, BS, G, NQ_, KST_, VST_>::TH
                     go = *abort_flag ? 0 : 1;
                 }
                 if (!__shfl_sync(FULL, go, 0)) break;
-                const int nb = min(BPT, nblk_seq - t * BPT);
+                const int tile = t_lo + t;                     // KV tile of the sequence
+                const int nb = min(BPT, nblk_seq - tile * BPT);
+                // blocks of the first tile that end before the window are not looked at (they may have
+                // been given away), rows there are masked
+                const int skip = Mod::kOn && t == 0 ? (tok_lo - tile * BN) / BS : 0;
                 const int phys = __shfl_sync(FULL, ecur, (t % TPB) * BPT + min(k, BPT - 1));
-                const bool mine = lane < nb * C::HALVES;
+                const bool mine = lane < nb * C::HALVES && (!Mod::kOn || k >= skip);
                 if (__any_sync(FULL, mine && (phys < 0 || phys >= p.num_blocks))) {
                     if (lane == 0) {
                         record_error(PA_DEVERR_BAD_BLOCK);
@@ -488,11 +514,13 @@ __global__ void __launch_bounds__(PrefillTcConfig<D, BS, G, NQ_, KST_, VST_>::TH
                     break;
                 }
                 // V tile holding rows past the context: the copy lands on v_tail, the rows past
-                // the context are zeroed, and only then is the tile marked full
-                const bool tail = is_v && (t + 1) * BN > ctx;
+                // the context are zeroed, and only then is the tile marked full (likewise the rows before
+                // the window)
+                const bool head = Mod::kOn && t == 0 && tok_lo > tile * BN;
+                const bool tail = is_v && ((tile + 1) * BN > ctx || head);
                 uint64_t *bar = tail ? v_tail : &full[st];
                 uint8_t *dst = smem + (is_v ? C::OFF_V : C::OFF_K) + st * C::KV_TILE;
-                if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(nb * C::HALVES * BS * 128));
+                if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)((nb - skip) * C::HALVES * BS * 128));
                 __syncwarp();
                 if (mine)
                     tma_load_2d(dst + hf * C::KV_HALF + k * BS * 128, map, hf * 64, (phys * p.h_kv + row_kvh) * BS, bar, pol);
@@ -502,7 +530,13 @@ __global__ void __launch_bounds__(PrefillTcConfig<D, BS, G, NQ_, KST_, VST_>::TH
                     const int landed = __shfl_sync(FULL, lane == 0 ? (int)mbar_wait_bounded(v_tail, ntail & 1) : 0, 0);
                     ++ntail;
                     if (landed) {
-                        const int r0 = ctx - t * BN, per_half = (BN - r0) * 8;
+                        if (Mod::kOn && head) {
+                            const int n8 = (tok_lo - tile * BN) * 8;
+                            for (int idx = lane; idx < C::HALVES * n8; idx += 32)
+                                *reinterpret_cast<uint4 *>(dst + (idx / n8) * C::KV_HALF + (idx % n8) * 16) =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        const int r0 = min(BN, ctx - tile * BN), per_half = (BN - r0) * 8;
                         for (int idx = lane; idx < C::HALVES * per_half; idx += 32) {
                             const int h = idx / per_half, rem = idx % per_half;
                             *reinterpret_cast<uint4 *>(dst + h * C::KV_HALF + (r0 + rem / 8) * 128 + (rem % 8) * 16) =
@@ -704,6 +738,17 @@ __global__ void __launch_bounds__(PrefillTcConfig<D, BS, G, NQ_, KST_, VST_>::TH
             const bool row_ok = tok < chunk;
             const int pos = row_ok ? ctx - chunk + tok : 0;
             const int first_pos = ctx - chunk + tok0;
+            // Mod: tokens [row_lo, row_hi] are what this row sees
+            const int kv_tile0 = first_token(chunk, ctx, it[IT_PAIR]) / BN;
+            int prefix = 0, row_lo = 0, row_hi = pos;
+            float slope = 0.f;
+            if constexpr (Mod::kOn) {
+                prefix = min(ctx, mod.prefix(it[IT_SEQ]));
+                row_lo = mod.first_token(pos);
+                row_hi = max(pos, prefix - 1);
+                slope = mod.slope(it[IT_KVH] * G + t % G);
+            }
+            const float qs = Mod::kOn ? 1.f : p.qk_scale;
             float m_run = -INFINITY, l_run = 0.f;
             bool failed = *abort_flag != 0;                    // a stopped CTA writes NaN rows
             for (int j = 0; j < nkv_q && !failed; ++j) {
@@ -724,8 +769,18 @@ __global__ void __launch_bounds__(PrefillTcConfig<D, BS, G, NQ_, KST_, VST_>::TH
 
                 // raw scores s; the log2-domain logit is s * qk_scale (qk_scale > 0, so the max of
                 // the logits is the scaled max of the scores), p = 2^(s * qk_scale - m) by one FMA
-                const int kv0 = j * BN;
-                if (kv0 + BN - 1 > first_pos) {
+                const int kv0 = (kv_tile0 + j) * BN;
+                if constexpr (Mod::kOn) {
+                    // log2-domain logits in place of the raw scores
+                    mod.logits(sr, p.qk_scale, slope, kv0 - pos, prefix > 0 && kv0 + BN - 1 > first_pos);
+                    if (kv0 + BN - 1 > max(first_pos, prefix - 1) || kv0 < mod.first_token(first_pos + C::TQ - 1)) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (kv0 + 32 * h + c > row_hi || kv0 + 32 * h + c < row_lo) sr[h][c] = 0xff800000u;
+                    }
+                } else if (kv0 + BN - 1 > first_pos) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -747,7 +802,7 @@ __global__ void __launch_bounds__(PrefillTcConfig<D, BS, G, NQ_, KST_, VST_>::TH
                 // l are rescaled) only when the tile's max exceeds it by more than 8, so p <= 2^8;
                 // O / l does not depend on the reference, and rescaling becomes rare, which keeps
                 // the softmax from waiting for the previous P V.
-                const float m_tile = mx * p.qk_scale;
+                const float m_tile = mx * qs;
                 float alpha = 1.f;
                 bool moved = false;
                 if (j == 0) {
@@ -757,12 +812,13 @@ __global__ void __launch_bounds__(PrefillTcConfig<D, BS, G, NQ_, KST_, VST_>::TH
                     m_run = m_tile;
                     moved = true;
                 }
-                const float mn = m_run;
+                // (a row that has seen no token yet, its window begins later: any finite reference gives 0)
+                const float mn = Mod::kOn && m_run == -INFINITY ? 0.f : m_run;
                 // p = 2^(s * qk_scale - m) in pairs: one packed FMA, then the MUFU unit for most pairs
                 // and the FMA-pipe polynomial for POLY_PAIRS of every 8 (the two units run side by
                 // side); the row sum in two packed partial sums
                 uint32_t pk[32];
-                const float2 sc2 = make_float2(p.qk_scale, p.qk_scale), nm2 = make_float2(-mn, -mn);
+                const float2 sc2 = make_float2(qs, qs), nm2 = make_float2(-mn, -mn);
                 float2 rsa = make_float2(0.f, 0.f), rsb = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
