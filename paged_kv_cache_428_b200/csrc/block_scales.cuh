@@ -43,18 +43,49 @@ __device__ __forceinline__ float block_scale_of(float amax)
 }
 
 template <int QT>
-__device__ __forceinline__ uint32_t encode4(float x0, float x1, float x2, float x3, float s)
+__device__ __forceinline__ uint32_t pack_codes(float x0, float x1, float x2, float x3)
 {
-    if (s == 0.f) return 0u;
-    x0 = __fdiv_rn(x0, s);
-    x1 = __fdiv_rn(x1, s);
-    x2 = __fdiv_rn(x2, s);
-    x3 = __fdiv_rn(x3, s);
     if constexpr (QT == 1) {
         return (uint32_t)float2_to_e4m3x2(x0, x1) | ((uint32_t)float2_to_e4m3x2(x2, x3) << 16);
     } else {
         return ((uint32_t)float_to_s8_sym(x0) & 0xffu) | (((uint32_t)float_to_s8_sym(x1) & 0xffu) << 8) |
                (((uint32_t)float_to_s8_sym(x2) & 0xffu) << 16) | ((uint32_t)float_to_s8_sym(x3) << 24);
+    }
+}
+
+// Codes of four values at scale s.
+template <int QT>
+__device__ __forceinline__ uint32_t encode4(float x0, float x1, float x2, float x3, float s)
+{
+    if (s == 0.f) return 0u;
+    return pack_codes<QT>(__fdiv_rn(x0, s), __fdiv_rn(x1, s), __fdiv_rn(x2, s), __fdiv_rn(x3, s));
+}
+
+// The same for finite values and a scale in [2^-100, 2^100], r = 1 / s rounded: the quotient by a product and
+// one residual step (as in Markstein's division), q1 = q0 + (x - q0 s) r.  The residual is exact, so q1 is
+// within a step of the quotient, and is the quotient where that is an fp32 number.  Ties between two codes are
+// fp32 numbers, and every other quotient of 8-bit significands is further than that from a tie: the codes
+// are those of the division, at 3 instructions a value instead of about 12 (prompts of 37k tokens: 131 us with the
+// division, see the kernel below for what it takes now).  INT8: |q| <= 127 by the choice of the scale, and adding
+// 1.5 * 2^23 rounds it to nearest, ties to even, into the low byte.
+template <int QT>
+__device__ __forceinline__ uint32_t encode4_fast(float x0, float x1, float x2, float x3, float s, float r)
+{
+    auto divide = [&](float x) {
+        const float q = x * r;
+        return fmaf(fmaf(-q, s, x), r, q);
+    };
+    x0 = divide(x0);
+    x1 = divide(x1);
+    x2 = divide(x2);
+    x3 = divide(x3);
+    if constexpr (QT == 1) {
+        return pack_codes<1>(x0, x1, x2, x3);
+    } else {
+        constexpr float R = 12582912.f;                // 1.5 * 2^23
+        const uint32_t a = __byte_perm(__float_as_uint(x0 + R), __float_as_uint(x1 + R), 0x0040);
+        const uint32_t b = __byte_perm(__float_as_uint(x2 + R), __float_as_uint(x3 + R), 0x0040);
+        return __byte_perm(a, b, 0x5410);
     }
 }
 
@@ -73,31 +104,33 @@ __device__ __forceinline__ uint32_t requantise4(uint32_t w, float was, float now
     return encode4<QT>(a.x * was, a.y * was, b.x * was, b.y * was, now);
 }
 
-__device__ __forceinline__ float finite_abs(float x)
-{
-    const float a = fabsf(x);
-    return a < INFINITY ? a : 0.f;                     // infinities and NaN take no part in the scale
-}
-
 constexpr int kScaleWriteWarps = 8;
 constexpr int kScaleWriteMaxChunk = 64;
 
+__device__ __forceinline__ void team_sync(int team, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(threads) : "memory");
+}
+
 // A run is a maximal stretch of tokens next to each other whose slots lie in one block.  A CTA looks after
-// the runs that begin in its `chunk` tokens, for `heads` KV heads; a warp takes one (run, head, K or V) at a
-// time: which token owns which row (the later one, if two have the same slot), maximum over the rows, the
-// scale, older rows requantised if it grew, the rows.
-template <int D, int BS, int QT>
+// the runs that begin in its `chunk` tokens, for `heads` KV heads.  First it finds for each run which token owns
+// which row of the block (the later one, if two have the same slot); then teams of TW warps take one (run, head,
+// K or V) at a time: the rows into registers, maximum over them, the scale, older rows requantised if it
+// grew, the rows' codes.  With TW = BS / (rows of 8 loads of a warp) a whole block is in the registers of its team
+// and its rows are read once; with TW = 1 (few tokens) a longer run's rows are read twice.
+template <int D, int BS, int QT, int TW>
 __global__ void __launch_bounds__(kScaleWriteWarps * 32) write_block_scales_kernel(const BlockScaleWriteParams p)
 {
     constexpr unsigned FULL = 0xffffffffu;
     constexpr int LPR = D / 8, RPI = 32 / LPR;         // lanes per bf16 row, rows of one load
-    constexpr int KEEP = 8;                            // loads kept in registers
+    constexpr int KEEP = 8, ROWS = TW * KEEP * RPI;    // loads kept in registers, rows of a team's loads
     constexpr int WINDOW = kScaleWriteMaxChunk + BS;   // tokens whose borders are looked at
     constexpr int WORDS = (WINDOW + 31) / 32;
     __shared__ uint32_t border[WORDS + 1];             // bit i: token t0 + i does not continue the run of t0 + i - 1
-    __shared__ int run_first[kScaleWriteMaxChunk];
+    __shared__ int run_first[kScaleWriteMaxChunk], run_lo[kScaleWriteMaxChunk], run_hi[kScaleWriteMaxChunk];
     __shared__ int num_runs;
-    __shared__ int owner_of[kScaleWriteWarps][BS];
+    __shared__ int owner_of[kScaleWriteMaxChunk][BS];
+    __shared__ uint32_t team_max[2][kScaleWriteWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long t0 = (long long)blockIdx.x * p.chunk;
 
@@ -119,14 +152,11 @@ __global__ void __launch_bounds__(kScaleWriteWarps * 32) write_block_scales_kern
             record_error(PA_DEVERR_BAD_SLOT);
     }
     __syncthreads();
-
-    const int h0 = blockIdx.y * p.heads, nh = min(p.heads, p.h_kv - h0);
-    const int items = num_runs * nh * 2;
-    for (int item = warp; item < items; item += kScaleWriteWarps) {
-        const bool is_v = item & 1;
-        const int h = h0 + (item >> 1) % nh, first_tok = run_first[(item >> 1) / nh];
+    for (int run = warp; run < num_runs; run += kScaleWriteWarps) {
+        const int first = run_first[run];
+        const long long blk = block_of(t0 + first);
         // the run's end: the next border, or (slots given twice) further on
-        int end = first_tok + 1;
+        int end = first + 1;
         for (;;) {
             const uint32_t w = border[end >> 5] >> (end & 31);
             if (w) {
@@ -136,16 +166,15 @@ __global__ void __launch_bounds__(kScaleWriteWarps * 32) write_block_scales_kern
             end = (end | 31) + 1;
             if (end >= window) break;
         }
-        const long long blk = block_of(t0 + first_tok);
         if (end >= window) {
             end = window;
             while (block_of(t0 + end) == blk) ++end;
         }
-        int *owner = owner_of[warp];
+        int *owner = owner_of[run];
         for (int i = lane; i < BS; i += 32) owner[i] = -1;
         __syncwarp();
         int lo = BS, hi = -1;
-        for (int i = first_tok + lane; i < end; i += 32) {
+        for (int i = first + lane; i < end; i += 32) {
             const int off = (int)(p.slot_mapping[t0 + i] - blk * BS);
             atomicMax(&owner[off], (int)(t0 + i));
             lo = min(lo, off);
@@ -153,44 +182,82 @@ __global__ void __launch_bounds__(kScaleWriteWarps * 32) write_block_scales_kern
         }
         lo = __reduce_min_sync(FULL, lo);
         hi = __reduce_max_sync(FULL, hi);
-        __syncwarp();
+        if (lane == 0) {
+            run_lo[run] = lo;
+            run_hi[run] = hi;
+        }
+    }
+    __syncthreads();
 
+    const int team = warp / TW, member = warp % TW;
+    const int sub = lane / LPR, col = lane % LPR;
+    const int h0 = blockIdx.y * p.heads, nh = min(p.heads, p.h_kv - h0);
+    const int items = num_runs * nh * 2;
+    int parity = 0;
+    for (int item = team; item < items; item += kScaleWriteWarps / TW, parity ^= 1) {
+        const bool is_v = item & 1;
+        const int h = h0 + (item >> 1) % nh, run = (item >> 1) / nh;
+        const int lo = run_lo[run], hi = run_hi[run];
+        const int *owner = owner_of[run];
+        const long long blk = block_of(t0 + run_first[run]);
         const __nv_bfloat16 *rows = (is_v ? p.value : p.key) + (size_t)h * D;
         const int64_t stride = is_v ? p.value_stride : p.key_stride;
         uint8_t *tile = (is_v ? p.v_cache : p.k_cache) + ((size_t)blk * p.h_kv + h) * BS * D;
         float *scale = (is_v ? p.v_scales : p.k_scales) + (size_t)blk * p.h_kv + h;
         const float was = lo > 0 ? *scale : 0.f;       // a block written from its first row on has no older rows
-        const int sub = lane / LPR, col = lane % LPR;
         uint4 v[KEEP];
-        // rows base + sub, base + sub + RPI, ... of the block, 8 elements of each
+        auto row_of = [&](int base, int k) { return base + (member * KEEP + k) * RPI + sub; };
         auto load = [&](int base) {
 #pragma unroll
             for (int k = 0; k < KEEP; ++k) {
-                const int row = base + k * RPI + sub;
-                const int t = row <= hi ? owner[row] : -1;
+                const int row = row_of(base, k), t = row <= hi ? owner[row] : -1;
                 v[k] = t >= 0 ? __ldg(reinterpret_cast<const uint4 *>(rows + t * stride) + col) : make_uint4(0, 0, 0, 0);
             }
         };
-        float amax = 0.f;
-        for (int base = lo; base <= hi; base += KEEP * RPI) {
+        // maximum of |x|: the bits of finite bf16 magnitudes order like integers, two at a time
+        uint32_t top = 0;
+        for (int base = lo; base <= hi; base += ROWS) {
             load(base);
 #pragma unroll
             for (int k = 0; k < KEEP; ++k) {
-                const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = bf16x2_to_float2(w[e]);
-                    amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
-                }
+                top = __vmaxu2(top, __vmaxu2(v[k].x & 0x7fff7fffu, v[k].y & 0x7fff7fffu));
+                top = __vmaxu2(top, __vmaxu2(v[k].z & 0x7fff7fffu, v[k].w & 0x7fff7fffu));
             }
         }
+        auto over_team = [&](uint32_t m, int slot) {   // the maximum over the team's threads
+            m = __reduce_max_sync(FULL, m);
+            if constexpr (TW > 1) {
+                if (lane == 0) team_max[slot][warp] = m;
+                team_sync(team, TW * 32);
 #pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, off));
-        const float now = fmaxf(was, block_scale_of<QT>(amax));
-        __syncwarp();                                  // every lane has read the old scale
+                for (int i = 0; i < TW; ++i) m = max(m, team_max[slot][team * TW + i]);
+            }
+            return m;
+        };
+        top = over_team(max(top & 0xffffu, top >> 16), parity);
+        const bool finite = top < 0x7f80u;
+        if (!finite) {                                 // infinities and NaN take no part: once more without them
+            if constexpr (TW > 1) team_sync(team, TW * 32);
+            uint32_t m = 0;
+            for (int base = lo; base <= hi; base += ROWS) {
+                load(base);
+#pragma unroll
+                for (int k = 0; k < KEEP; ++k) {
+                    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t a = (w[e >> 1] >> (16 * (e & 1))) & 0x7fffu;
+                        m = a < 0x7f80u ? max(m, a) : m;
+                    }
+                }
+            }
+            top = over_team(m, parity);
+        }
+        const float now = fmaxf(was, block_scale_of<QT>(__uint_as_float(top << 16)));
+        __syncwarp();                                  // (the team's barrier) every lane has read the old scale
         if (lo > 0 && now > was) {
             // the scale grew: the rows before the first new one move to it (16 codes at a time)
-            for (int i = lane; i < lo * (D / 16); i += 32) {
+            for (int i = member * 32 + lane; i < lo * (D / 16); i += TW * 32) {
                 uint4 c = reinterpret_cast<uint4 *>(tile)[i];
                 c.x = requantise4<QT>(c.x, was, now);
                 c.y = requantise4<QT>(c.y, was, now);
@@ -199,22 +266,27 @@ __global__ void __launch_bounds__(kScaleWriteWarps * 32) write_block_scales_kern
                 reinterpret_cast<uint4 *>(tile)[i] = c;
             }
         }
-        if (lane == 0) *scale = now;
-        const bool kept = hi - lo < KEEP * RPI;        // the rows are still in registers
-        for (int base = lo; base <= hi; base += KEEP * RPI) {
+        if (member == 0 && lane == 0) *scale = now;
+        const bool fast = finite && now >= 0x1p-100f && now <= 0x1p100f;
+        const float r = __frcp_rn(now);
+        const bool kept = hi - lo < ROWS;              // the rows are still in registers
+        for (int base = lo; base <= hi; base += ROWS) {
             if (!kept) load(base);
 #pragma unroll
             for (int k = 0; k < KEEP; ++k) {
-                const int row = base + k * RPI + sub;
+                const int row = row_of(base, k);
                 if (row <= hi && owner[row] >= 0) {
                     const float2 a = bf16x2_to_float2(v[k].x), b = bf16x2_to_float2(v[k].y);
                     const float2 c = bf16x2_to_float2(v[k].z), d = bf16x2_to_float2(v[k].w);
-                    reinterpret_cast<uint2 *>(tile + (size_t)row * D)[col] =
-                        make_uint2(encode4<QT>(a.x, a.y, b.x, b.y, now), encode4<QT>(c.x, c.y, d.x, d.y, now));
+                    uint2 code;
+                    if (fast)
+                        code = make_uint2(encode4_fast<QT>(a.x, a.y, b.x, b.y, now, r), encode4_fast<QT>(c.x, c.y, d.x, d.y, now, r));
+                    else
+                        code = make_uint2(encode4<QT>(a.x, a.y, b.x, b.y, now), encode4<QT>(c.x, c.y, d.x, d.y, now));
+                    reinterpret_cast<uint2 *>(tile + (size_t)row * D)[col] = code;
                 }
             }
         }
-        __syncwarp();                                  // owner free for the next item
     }
 }
 

@@ -131,7 +131,6 @@ struct EvictParams {
     int max_blocks, new_max_blocks;
     int h_kv, block_size, num_blocks;
     int budget, recent;
-    int slice_cap;                 // weights of one CTA that fit its shared memory
 };
 
 // What becomes of a sequence of ctx tokens: `older` of them compete for `need` places, the `last` ones stay.
@@ -149,177 +148,230 @@ struct EvictCounts {
     }
 };
 
-// Order of the weights as unsigned numbers; what is not above 0 (NaN included) ranks as 0.
-__device__ __forceinline__ uint32_t weight_key(float w) { return w > 0.f ? __float_as_uint(w) : 0u; }
+// Order of the weights as whole numbers; what is not above 0 (NaN included) ranks as 0.
+__device__ __forceinline__ int weight_key(float w) { return w > 0.f ? __float_as_int(w) : 0; }
 
-constexpr int kSelectThreads = 512, kSelectWarps = kSelectThreads / 32;
 constexpr int kSelectBins = 2048;
 constexpr int kSelectMaxCluster = 8;
-constexpr int kSelectSlice = 16384;                    // weights that one CTA keeps in shared memory
 
-// One cluster for each (sequence, KV head); its CTAs hold slices of the row of weights in shared memory (or
-// read them again from L2 where the row is longer than 8 slices).  The need-th largest key comes out of three
-// passes over 11, 11 and 10 bits of it: a histogram of the keys that agree with the digits so far, added up over
-// the cluster, and the digit in which the remaining count runs out.  Equal keys are taken from the front, by
-// their rank among equals.  All counts are integers: the choice does not depend on timing.
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictParams p)
+// One cluster for each (sequence, KV head); its CTAs take slices of the row of weights.  Warp w of a CTA holds
+// V x 32 neighbouring keys of its slice in registers (a row longer than NT * V keys for each CTA is read again,
+// NT * V at a time, for every step below); -1 stands for no key.  The need-th largest key comes out of three
+// passes over its upper 11, next 11 and last 10 bits: a histogram of the keys that agree with the digits so far,
+// and the digit in which the remaining count runs out.  To find it the first warp of every CTA adds up, over
+// the cluster, 32 sums of neighbouring bins, then the bins behind one of them (all bins of all CTAs would keep the
+// paths between the SMs busy for longer than the rest takes).  Equal keys are taken from the front, by their
+// rank among equals.  All counts are integers: the choice does not depend on timing.
+//   Bound by instructions and barriers, not by the row's 4 bytes a token.
+template <int NT, int V>
+__global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const EvictParams p)
 {
     namespace cg = cooperative_groups;
     constexpr unsigned FULL = 0xffffffffu;
-    extern __shared__ uint32_t keys[];                 // [slice_cap]
-    __shared__ int hist[kSelectBins];
-    __shared__ int warp_sum[kSelectWarps];
-    __shared__ int found[2];                           // digit, keys in the digits above it
+    constexpr int NWARP = NT / 32;
+    __shared__ __align__(16) int hist[3][kSelectBins];
+    __shared__ int coarse[3][32];                      // sums of bins / 32 neighbouring bins
+    __shared__ int found[3][2];                        // of each pass: the digit, keys in the digits above it
     __shared__ int counts[2];                          // this CTA's keys above the threshold, and equal to it
-    __shared__ int warp_gt[kSelectWarps], warp_eq[kSelectWarps];
+    __shared__ int warp_gt[NWARP], warp_eq[NWARP];
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = blockIdx.x, ranks = gridDim.x, kvh = blockIdx.y, seq = blockIdx.z;   // one cluster in x
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    pdl_launch_dependents();                           // the rows' copy may be set up meanwhile
     const EvictCounts n(p, seq);
     const size_t row = (size_t)seq * p.h_kv + kvh;
     const float *w = p.weights + row * p.stride;
     int32_t *kept = p.kept + row * p.budget;
     float *new_w = p.new_weights + row * p.new_stride;
+    const bool choose = n.need != n.older && n.need > 0;        // else nobody goes, or only the last ones stay
+    const int slice = (n.older + ranks - 1) / ranks;
+    const int first = min(n.older, rank * slice), len = choose ? min(n.older, first + slice) - first : 0;
+    const int chunks = choose ? (slice + NT * V - 1) / (NT * V) : 0;   // the same in every CTA of the cluster
+
+    int key[V], diff = 0;                              // diff: bits in which the lane's keys differ
+    int i0 = 0;                                        // place of key[0] of this lane in the slice
+    auto load = [&](int chunk) {
+        i0 = (chunk * NWARP + warp) * V * 32 + lane;
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = i0 + v * 32 < len ? weight_key(__ldg(w + first + i0 + v * 32)) : -1;
+        diff = 0;
+#pragma unroll
+        for (int v = 1; v < V; ++v) diff |= key[v] ^ key[0];
+    };
+    if (chunks == 1) load(0);
+    if (choose) {
+#pragma unroll
+        for (int h = 0; h < 3; ++h)
+            for (int b = tid; b < kSelectBins / 4; b += NT) reinterpret_cast<int4 *>(hist[h])[b] = make_int4(0, 0, 0, 0);
+    }
     if (kvh == 0 && rank == 0 && tid == 0) {
         p.new_lens[seq] = n.size;
         if (__ldg(p.context_lens + seq) > p.stride) record_error(PA_DEVERR_BAD_LENGTH);
     }
     // what needs no choice: the last ones, and the end of the rows
-    const int all = rank * kSelectThreads + tid, step = ranks * kSelectThreads;
+    const int all = rank * NT + tid, step = ranks * NT;
     for (int j = all; j < n.last; j += step) {
         kept[n.need + j] = n.older + j;
-        new_w[n.need + j] = w[n.older + j];
+        new_w[n.need + j] = __ldg(w + n.older + j);
     }
     for (int j = n.size + all; j < p.budget; j += step) kept[j] = -1;
     for (int64_t j = n.size + all; j < p.new_stride; j += step) new_w[j] = 0.f;
-    if (n.need == n.older) {                           // nobody goes
+    if (!choose) {                                     // the whole cluster
         for (int j = all; j < n.need; j += step) {
             kept[j] = j;
-            new_w[j] = w[j];
+            new_w[j] = __ldg(w + j);
         }
-        return;                                        // the whole cluster
+        return;
     }
-    if (n.need == 0) return;
+    __syncthreads();
 
-    const int slice = (n.older + ranks - 1) / ranks;
-    const int first = min(n.older, rank * slice), len = min(n.older, first + slice) - first;
-    const bool in_smem = slice <= p.slice_cap;
-    if (in_smem)
-        for (int i = tid; i < len; i += kSelectThreads) keys[i] = weight_key(__ldg(w + first + i));
-    auto key_at = [&](int i) { return in_smem ? keys[i] : weight_key(__ldg(w + first + i)); };
-
-    uint32_t prefix = 0, mask = 0;
+    int prefix = 0, mask = 0;
     int remaining = n.need;
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
-        for (int b = tid; b < bins; b += kSelectThreads) hist[b] = 0;
-        __syncthreads();
-        for (int i0 = warp * 32; i0 < len; i0 += kSelectThreads) {
-            const int i = i0 + lane;
-            const uint32_t k = i < len ? key_at(i) : 0u;
-            const bool in = i < len && (k & mask) == prefix;
-            const int bin = in ? (int)((k >> shift) & (bins - 1)) : -1;
+        // a key's first digit is below 1024 (its sign bit is 0); -1 goes to bin 2047, which nobody reads
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, digits = pass == 2 ? 1023 : 2047, bins = pass == 1 ? 2048 : 1024;
+        for (int chunk = 0; chunk < chunks; ++chunk) {
+            if (chunks > 1) load(chunk);
             // a warp of equal digits (weights that are all alike) adds once
-            int same = 0;
-            __match_all_sync(FULL, bin, &same);
-            if (same) {
-                if (in && lane == 0) atomicAdd(&hist[bin], 32);
-            } else if (in) {
-                atomicAdd(&hist[bin], 1);
+            const int cared = mask | (digits << shift);
+            if (__all_sync(FULL, ((diff | (key[0] ^ __shfl_sync(FULL, key[0], 0))) & cared) == 0)) {
+                if (lane == 0 && (key[0] & mask) == prefix) atomicAdd(&hist[pass][(key[0] >> shift) & digits], 32 * V);
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if ((key[v] & mask) == prefix) atomicAdd(&hist[pass][(key[v] >> shift) & digits], 1);
             }
         }
         __syncthreads();
+        const int width = bins / 32;                   // 32 or 64
+        for (int b = warp; b < 32; b += NWARP) {
+            const int *from = hist[pass] + b * width + lane;
+            const int sum = __reduce_add_sync(FULL, width == 64 ? from[0] + from[32] : from[0]);
+            if (lane == 0) coarse[pass][b] = sum;
+        }
         if (ranks > 1) cluster.sync();
-        // thread t has bins 4 t .. 4 t + 3, counted from the top
-        int c[4], sum = 0;
+        else __syncthreads();
+        if (warp == 0) {
+            auto over_cluster = [&](const int *at) {
+                int sum = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int b = bins - 1 - (4 * tid + j);
-            c[j] = 0;
-            if (b >= 0) {
-                if (ranks == 1) c[j] = hist[b];
-                else
-                    for (int r = 0; r < ranks; ++r) c[j] += *cluster.map_shared_rank(&hist[b], r);
-            }
-            sum += c[j];
-        }
-        int upto = sum;
+                for (int r = 0; r < kSelectMaxCluster; ++r)
+                    if (r < ranks) sum += ranks > 1 ? *cluster.map_shared_rank(at, r) : *at;
+                return sum;
+            };
+            // lane l: what lies above its (31 - l)-th stretch of values c; the lane in which `left` runs out
+            auto runs_out = [&](int c, int left, int &above) {
+                int upto = c;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(FULL, upto, off);
-            if (lane >= off) upto += y;
-        }
-        if (lane == 31) warp_sum[warp] = upto;
-        __syncthreads();
-        int above = upto - sum;
-        for (int i = 0; i < warp; ++i) above += warp_sum[i];
-        if (above < remaining && above + sum >= remaining) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (above < remaining && above + c[j] >= remaining) {
-                    found[0] = bins - 1 - (4 * tid + j);
-                    found[1] = above;
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int y = __shfl_up_sync(FULL, upto, off);
+                    if (lane >= off) upto += y;
                 }
-                above += c[j];
+                above = upto - c;
+                return __ffs(__ballot_sync(FULL, above < left && upto >= left)) - 1;
+            };
+            int above, more;
+            const int a = runs_out(over_cluster(&coarse[pass][31 - lane]), remaining, above);
+            const int before = __shfl_sync(FULL, above, a), left = remaining - before;
+            const int *fine = hist[pass] + (31 - a) * width;
+            if (width == 64) {
+                const int hi = over_cluster(fine + 63 - 2 * lane), lo = over_cluster(fine + 62 - 2 * lane);
+                const int b = runs_out(hi + lo, left, more);
+                const int c = __shfl_sync(FULL, hi, b), m = __shfl_sync(FULL, more, b);
+                const bool second = m + c < left;
+                if (lane == 0) {
+                    found[pass][0] = (31 - a) * 64 + 63 - 2 * b - second;
+                    found[pass][1] = before + m + (second ? c : 0);
+                }
+            } else {
+                const int b = runs_out(over_cluster(fine + 31 - lane), left, more);
+                if (lane == b) {
+                    found[pass][0] = (31 - a) * 32 + 31 - b;
+                    found[pass][1] = before + more;
+                }
             }
         }
         __syncthreads();
-        prefix |= (uint32_t)found[0] << shift;
-        mask |= (uint32_t)(bins - 1) << shift;
-        remaining -= found[1];
-        if (ranks > 1) cluster.sync();                 // every CTA has read the histograms
+        prefix |= found[pass][0] << shift;
+        mask |= digits << shift;
+        remaining -= found[pass][1];
     }
 
-    // ---- the kept ones in order: warp w has a stretch of the slice ----
-    const int part = (len + kSelectWarps - 1) / kSelectWarps;
-    const int i_begin = min(len, warp * part), i_end = min(len, i_begin + part);
-    int gt = 0, eq = 0;
-    for (int i0 = i_begin; i0 < i_end; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t k = i < i_end ? key_at(i) : 0u;
-        gt += __popc(__ballot_sync(FULL, i < i_end && k > prefix));
-        eq += __popc(__ballot_sync(FULL, i < i_end && k == prefix));
-    }
-    if (lane == 0) {
-        warp_gt[warp] = gt;
-        warp_eq[warp] = eq;
-    }
-    __syncthreads();
-    if (tid == 0) {
-        int a = 0, b = 0;
-        for (int i = 0; i < kSelectWarps; ++i) {
-            a += warp_gt[i];
-            b += warp_eq[i];
+    // ---- the kept ones, in order ----
+    // keys above the threshold and equal to it: of this warp's part of a chunk, of the CTA, of the CTAs before
+    auto count = [&](int &gt, int &eq) {
+        gt = eq = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            gt += key[v] > prefix;
+            eq += key[v] == prefix;
         }
-        counts[0] = a;
-        counts[1] = b;
-    }
-    if (ranks > 1) cluster.sync();
-    int gt_before = 0, eq_before = 0;
-    for (int r = 0; r < rank; ++r) {
-        gt_before += *cluster.map_shared_rank(&counts[0], r);
-        eq_before += *cluster.map_shared_rank(&counts[1], r);
-    }
-    for (int i = 0; i < warp; ++i) {
-        gt_before += warp_gt[i];
-        eq_before += warp_eq[i];
+        gt = __reduce_add_sync(FULL, gt);
+        eq = __reduce_add_sync(FULL, eq);
+    };
+    int gt = 0, eq = 0, gt_before = 0, eq_before = 0;
+    if (ranks > 1) {
+        int a = 0, b = 0;
+        for (int chunk = 0; chunk < chunks; ++chunk) {
+            if (chunks > 1) load(chunk);
+            count(gt, eq);
+            a += gt;
+            b += eq;
+        }
+        if (lane == 0) {
+            warp_gt[warp] = a;
+            warp_eq[warp] = b;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            a = __reduce_add_sync(FULL, lane < NWARP ? warp_gt[lane] : 0);
+            b = __reduce_add_sync(FULL, lane < NWARP ? warp_eq[lane] : 0);
+            if (lane == 0) {
+                counts[0] = a;
+                counts[1] = b;
+            }
+        }
+        cluster.sync();
+        const bool mine = lane < rank;
+        gt_before = __reduce_add_sync(FULL, mine ? *cluster.map_shared_rank(&counts[0], mine ? lane : 0) : 0);
+        eq_before = __reduce_add_sync(FULL, mine ? *cluster.map_shared_rank(&counts[1], mine ? lane : 0) : 0);
     }
     const uint32_t below = (1u << lane) - 1u;
-    for (int i0 = i_begin; i0 < i_end; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t k = i < i_end ? key_at(i) : 0u;
-        const uint32_t g = __ballot_sync(FULL, i < i_end && k > prefix), e = __ballot_sync(FULL, i < i_end && k == prefix);
-        const int g_pre = gt_before + __popc(g & below), e_pre = eq_before + __popc(e & below);
-        if (i < i_end && (k > prefix || (k == prefix && e_pre < remaining))) {
-            const int at = g_pre + min(e_pre, remaining);
-            kept[at] = first + i;
-            new_w[at] = __ldg(w + first + i);
+    for (int chunk = 0; chunk < chunks; ++chunk) {
+        if (chunks > 1) load(chunk);
+        if (chunks > 1 || ranks == 1) count(gt, eq);
+        if (chunks > 1 || ranks == 1) {
+            __syncthreads();                           // the previous chunk's counts have been read
+            if (lane == 0) {
+                warp_gt[warp] = gt;
+                warp_eq[warp] = eq;
+            }
+            __syncthreads();
         }
-        gt_before += __popc(g);
-        eq_before += __popc(e);
+        int g_at = gt_before + __reduce_add_sync(FULL, lane < warp ? warp_gt[lane] : 0);
+        int e_at = eq_before + __reduce_add_sync(FULL, lane < warp ? warp_eq[lane] : 0);
+        if (chunks > 1) {
+            gt_before += __reduce_add_sync(FULL, lane < NWARP ? warp_gt[lane] : 0);
+            eq_before += __reduce_add_sync(FULL, lane < NWARP ? warp_eq[lane] : 0);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const uint32_t g = __ballot_sync(FULL, key[v] > prefix), e = __ballot_sync(FULL, key[v] == prefix);
+            if (g | e) {
+                const int g_pre = g_at + __popc(g & below), e_pre = e_at + __popc(e & below);
+                if (key[v] > prefix || (key[v] == prefix && e_pre < remaining)) {
+                    const int at = g_pre + min(e_pre, remaining), i = first + i0 + v * 32;
+                    kept[at] = i;
+                    // what is above 0 is its key; below that the weight itself
+                    new_w[at] = key[v] ? __int_as_float(key[v]) : __ldg(w + i);
+                }
+                g_at += __popc(g);
+                e_at += __popc(e);
+            }
+        }
     }
-    if (ranks > 1) cluster.sync();                     // `counts` read by every CTA before any of them leaves
+    if (ranks > 1) cluster.sync();                     // histograms and counts read by every CTA before any leaves
 }
 
 // ---- moving the rows ------------------------------------------------------------------------------
@@ -333,6 +385,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const Evict
     constexpr int RPW = 32 / LPR, U = 4, ROWS = RPW * U;       // rows of a warp
     const int kvh = blockIdx.y, seq = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const EvictCounts n(p, seq);
+    pdl_wait();                                                // the choice is complete
     const int j0 = (blockIdx.x * kMoveWarps + warp) * ROWS + lane / LPR;
     const int col = lane % LPR;
     if ((int)(blockIdx.x * kMoveWarps + warp) * ROWS >= n.size) return;

@@ -10,11 +10,19 @@ namespace {
 
 bool quantised(int cache_dtype) { return cache_dtype == PA_CACHE_E4M3 || cache_dtype == PA_CACHE_INT8; }
 
+template <int D, int BS, int TW>
+void launch_write_team(int cache_dtype, dim3 grid, const BlockScaleWriteParams &p, cudaStream_t st)
+{
+    if (cache_dtype == PA_CACHE_E4M3) write_block_scales_kernel<D, BS, 1, TW><<<grid, kScaleWriteWarps * 32, 0, st>>>(p);
+    else write_block_scales_kernel<D, BS, 2, TW><<<grid, kScaleWriteWarps * 32, 0, st>>>(p);
+}
+
 template <int D, int BS>
 void launch_write(int cache_dtype, dim3 grid, const BlockScaleWriteParams &p, cudaStream_t st)
 {
-    if (cache_dtype == PA_CACHE_E4M3) write_block_scales_kernel<D, BS, 1><<<grid, kScaleWriteWarps * 32, 0, st>>>(p);
-    else write_block_scales_kernel<D, BS, 2><<<grid, kScaleWriteWarps * 32, 0, st>>>(p);
+    constexpr int WHOLE = cmax(1, BS * D / 8 / 32 / 8);        // warps whose 8 loads each are a whole block
+    if (p.chunk == kScaleWriteMaxChunk) launch_write_team<D, BS, WHOLE>(cache_dtype, grid, p, st);
+    else launch_write_team<D, BS, 1>(cache_dtype, grid, p, st);
 }
 
 template <int D>

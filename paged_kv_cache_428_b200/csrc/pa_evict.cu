@@ -16,37 +16,40 @@ size_t logit_bytes(int num_seqs, int h_q, int max_context_len)
     return round256((size_t)num_seqs * h_q * logit_tokens(max_context_len) * sizeof(float));
 }
 
-int launch_select(const EvictParams &p, int num_seqs, int max_context_len, cudaStream_t st)
+template <int NT, int V>
+int launch_select_as(const EvictParams &p, int num_seqs, int ranks, cudaStream_t st)
 {
-    // CTAs of a cluster: one for each slice of the longest row
-    int ranks = 1;
-    while (ranks < kSelectMaxCluster && (long long)ranks * kSelectSlice / 2 < max_context_len) ranks *= 2;
-    const int slice = (max_context_len + ranks - 1) / ranks;
-    EvictParams q = p;
-    q.slice_cap = slice <= kSelectSlice ? (slice + 255) / 256 * 256 : 0;
-    static std::atomic<unsigned long long> smem_set{0};
-    const int rc = allow_smem(evict_select_kernel, kSelectSlice * (int)sizeof(uint32_t), smem_set);
-    if (rc != PA_OK) return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ranks, p.h_kv, num_seqs);
-    cfg.blockDim = dim3(kSelectThreads);
-    cfg.dynamicSmemBytes = (size_t)q.slice_cap * sizeof(uint32_t);
+    cfg.blockDim = dim3(NT);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = ranks;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, evict_select_kernel, q) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    cfg.numAttrs = ranks > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, evict_select_kernel<NT, V>, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// Keys of a row in the registers of as few threads as hold them: 4096 a CTA of 256 threads up to clusters of 8,
+// 16384 a CTA of 512 beyond.  More threads a CTA are faster alone but fill the SMs: 512 rows of up to 4096 in two
+// waves, 24.6 us at 512 threads; 16 clusters of 8 for 131072 in two waves, 50 us at 1024.
+int launch_select(const EvictParams &p, int num_seqs, int max_context_len, cudaStream_t st)
+{
+    int ranks = 1;
+    while (ranks < kSelectMaxCluster && ranks * 4096 < max_context_len) ranks *= 2;
+    if (max_context_len <= 1024) return launch_select_as<256, 4>(p, num_seqs, 1, st);
+    if (max_context_len <= kSelectMaxCluster * 4096) return launch_select_as<256, 16>(p, num_seqs, ranks, st);
+    return launch_select_as<512, 32>(p, num_seqs, kSelectMaxCluster, st);
 }
 
 template <int LPR>
 int launch_move(const EvictParams &p, int num_seqs, int most, cudaStream_t st)
 {
     const int rows = 32 / LPR * 4 * kMoveWarps;
-    evict_move_kernel<LPR><<<dim3((most + rows - 1) / rows, p.h_kv, num_seqs), kMoveWarps * 32, 0, st>>>(p);
-    return launch_status();
+    return launch_ex(evict_move_kernel<LPR>, dim3((most + rows - 1) / rows, p.h_kv, num_seqs), dim3(kMoveWarps * 32), 0, st,
+                     true, p);
 }
 
 bool overlap(const void *a, size_t an, const void *b, size_t bn)
