@@ -363,8 +363,8 @@ int pa_decode_scoremod(void *out, const void *q, const void *k_cache, const void
                        const float *alibi_slopes, int window, int cache_dtype, void *workspace, size_t workspace_bytes,
                        void *stream);
 
-/* pa_prefill_scoremod: arguments, workspace (pa_prefill_workspace_size bytes) and errors as pa_prefill_ws, but
- * scale may have any sign.  Rows of one chunk are worked on in tiles: V of tokens that some rows of a tile see
+/* pa_prefill_scoremod: arguments, workspace (pa_prefill_workspace_size bytes) and errors as pa_prefill_ws, and
+ * scale is at least 2^-64 (else PA_ERR_INVALID_ARG).  Rows of one chunk are worked on in tiles: V of tokens that some rows of a tile see
  * and others do not must be finite (as in pa_prefill). */
 int pa_prefill_scoremod(void *out, const void *q, const void *k_cache, const void *v_cache, const int32_t *block_tables,
                         int max_blocks_per_seq, const int32_t *query_start, const int32_t *context_lens, int num_seqs,

@@ -11,22 +11,44 @@ namespace {
 
 bool valid_softcap(float cap) { return std::isfinite(cap) && cap >= 0.f; }
 
-template <int D, int BS>
-int dispatch_scoremod_group(int g, const PrefillParams &pp, int n, int mql, int *counters, const PrefillScoreMod &mod,
-                            cudaStream_t st)
+template <int D, int BS, bool CAP, bool BIAS>
+int dispatch_scoremod_group(int g, const PrefillParams &pp, int n, int mql, int *counters,
+                            const PrefillScoreMod<CAP, BIAS> &mod, cudaStream_t st)
 {
     return switch_group(g, [&](auto gc) {
-        return launch_prefill_tc<D, BS, decltype(gc)::value, PrefillScoreMod>(pp, n, mql, counters, st, mod);
+        return launch_prefill_tc<D, BS, decltype(gc)::value, PrefillScoreMod<CAP, BIAS>>(pp, n, mql, counters, st, mod);
     });
 }
 
-template <int D>
-int dispatch_scoremod(int bs, int g, const PrefillParams &pp, int n, int mql, int *counters, const PrefillScoreMod &mod,
-                      cudaStream_t st)
+template <int D, bool CAP, bool BIAS>
+int dispatch_scoremod_block(int bs, int g, const PrefillParams &pp, int n, int mql, int *counters,
+                            const PrefillScoreMod<CAP, BIAS> &mod, cudaStream_t st)
 {
     if (bs == 16) return dispatch_scoremod_group<D, 16>(g, pp, n, mql, counters, mod, st);
     if (bs == 32) return dispatch_scoremod_group<D, 32>(g, pp, n, mql, counters, mod, st);
     return dispatch_scoremod_group<D, 64>(g, pp, n, mql, counters, mod, st);
+}
+
+template <bool CAP, bool BIAS>
+int dispatch_scoremod(int d, int bs, int g, const PrefillParams &pp, int n, int mql, int *counters, float scale, float softcap,
+                      const float *slopes, int window, const int32_t *prefix_lens, cudaStream_t st)
+{
+    PrefillScoreMod<CAP, BIAS> mod{};
+    mod.slopes = slopes;
+    mod.prefix_lens = prefix_lens;
+    mod.window = window;
+    if (CAP) {
+        // y = raw score * in; logit = out * y q(y^2)
+        const double in = (double)scale / softcap, to = (double)softcap * kLog2e;
+        const double coef[3] = {PA_TANH_C0, PA_TANH_C1, PA_TANH_C2};
+        mod.cap_in = (float)(2. * in * kLog2e);
+        mod.cap_out = (float)to;
+        mod.range = (float)(PA_TANH_RANGE / in);
+        double f = to * in;
+        for (int i = 0; i < 3; ++i, f *= in * in) mod.c[i] = (float)(coef[i] * f);
+    }
+    return d == 64 ? dispatch_scoremod_block<64>(bs, g, pp, n, mql, counters, mod, st)
+                   : dispatch_scoremod_block<128>(bs, g, pp, n, mql, counters, mod, st);
 }
 
 }  // namespace
@@ -64,7 +86,7 @@ int pa_prefill_scoremod(void *out, const void *q, const void *k_cache, const voi
 {
     if (workspace == nullptr || workspace_bytes < kPrefillWorkspaceBytes || !aligned16(workspace)) return PA_ERR_WORKSPACE;
     if (num_seqs < 0 || max_query_len < 0 || h_q <= 0 || h_kv <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 || window < 0 ||
-        h_q % h_kv != 0 || !std::isfinite(scale) || !valid_softcap(softcap) || cache_dtype < PA_CACHE_BF16 ||
+        h_q % h_kv != 0 || !std::isfinite(scale) || scale < 0x1p-64f || !valid_softcap(softcap) || cache_dtype < PA_CACHE_BF16 ||
         cache_dtype > PA_CACHE_INT8)
         return PA_ERR_INVALID_ARG;
     if (cache_dtype != PA_CACHE_BF16) return PA_ERR_UNSUPPORTED;
@@ -87,24 +109,13 @@ int pa_prefill_scoremod(void *out, const void *q, const void *k_cache, const voi
     pp.h_kv = h_kv;
     pp.num_blocks = num_blocks;
     pp.qk_scale = scale * kLog2e;
-    PrefillScoreMod mod{};
-    mod.slopes = alibi_slopes;
-    mod.prefix_lens = prefix_lens;
-    mod.window = window;
-    if (softcap > 0.f) {
-        // y = raw score * in; logit = out * y q(y^2)
-        const double in = (double)scale / softcap, to = (double)softcap * kLog2e;
-        const double coef[5] = {PA_TANH_C0, PA_TANH_C1, PA_TANH_C2, PA_TANH_C3, PA_TANH_C4};
-        mod.cap_in = (float)(2. * in * kLog2e);
-        mod.cap_out = (float)to;
-        mod.range = in != 0. ? (float)(PA_TANH_RANGE / std::fabs(in)) : INFINITY;
-        double f = to * in;
-        for (int i = 0; i < 5; ++i, f *= in * in) mod.c[i] = (float)(coef[i] * f);
-    }
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    int *counters = static_cast<int *>(workspace);
-    return head_dim == 64 ? dispatch_scoremod<64>(block_size, h_q / h_kv, pp, num_seqs, max_query_len, counters, mod, st)
-                          : dispatch_scoremod<128>(block_size, h_q / h_kv, pp, num_seqs, max_query_len, counters, mod, st);
+    const auto run = [&](auto cap, auto bias) {
+        return dispatch_scoremod<decltype(cap)::value, decltype(bias)::value>(
+            head_dim, block_size, h_q / h_kv, pp, num_seqs, max_query_len, static_cast<int *>(workspace), scale, softcap,
+            alibi_slopes, window, prefix_lens, static_cast<cudaStream_t>(stream));
+    };
+    if (softcap > 0.f) return alibi_slopes ? run(std::true_type{}, std::true_type{}) : run(std::true_type{}, std::false_type{});
+    return alibi_slopes ? run(std::false_type{}, std::true_type{}) : run(std::false_type{}, std::false_type{});
 }
 
 }  // extern "C"

@@ -738,17 +738,13 @@ __global__ void __launch_bounds__(PrefillTcConfig<D, BS, G, NQ_, KST_, VST_>::TH
             const bool row_ok = tok < chunk;
             const int pos = row_ok ? ctx - chunk + tok : 0;
             const int first_pos = ctx - chunk + tok0;
-            // Mod: tokens [row_lo, row_hi] are what this row sees
             const int kv_tile0 = first_token(chunk, ctx, it[IT_PAIR]) / BN;
-            int prefix = 0, row_lo = 0, row_hi = pos;
+            int prefix = 0;                                    // Mod: tokens below it are seen by every row
             float slope = 0.f;
             if constexpr (Mod::kOn) {
                 prefix = min(ctx, mod.prefix(it[IT_SEQ]));
-                row_lo = mod.first_token(pos);
-                row_hi = max(pos, prefix - 1);
-                slope = mod.slope(it[IT_KVH] * G + t % G);
+                slope = mod.slope(it[IT_KVH] * G + t % G, p.qk_scale);
             }
-            const float qs = Mod::kOn ? 1.f : p.qk_scale;
             float m_run = -INFINITY, l_run = 0.f;
             bool failed = *abort_flag != 0;                    // a stopped CTA writes NaN rows
             for (int j = 0; j < nkv_q && !failed; ++j) {
@@ -770,15 +766,19 @@ __global__ void __launch_bounds__(PrefillTcConfig<D, BS, G, NQ_, KST_, VST_>::TH
                 // raw scores s; the log2-domain logit is s * qk_scale (qk_scale > 0, so the max of
                 // the logits is the scaled max of the scores), p = 2^(s * qk_scale - m) by one FMA
                 const int kv0 = (kv_tile0 + j) * BN;
+                float qs = p.qk_scale, off = 0.f;
                 if constexpr (Mod::kOn) {
-                    // log2-domain logits in place of the raw scores
-                    mod.logits(sr, p.qk_scale, slope, kv0 - pos, prefix > 0 && kv0 + BN - 1 > first_pos);
+                    // log2-domain logits are then sr * qs + off
+                    qs = mod.unit(p.qk_scale);
+                    off = mod.logits(sr, slope, kv0 - pos, prefix > 0 && kv0 + BN - 1 > first_pos) * qs;
                     if (kv0 + BN - 1 > max(first_pos, prefix - 1) || kv0 < mod.first_token(first_pos + C::TQ - 1)) {
+                        // the row sees tokens row_lo .. row_hi
+                        const int row_lo = mod.first_token(pos) - kv0, row_hi = max(pos, prefix - 1) - kv0;
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
-                                if (kv0 + 32 * h + c > row_hi || kv0 + 32 * h + c < row_lo) sr[h][c] = 0xff800000u;
+                                if (32 * h + c > row_hi || 32 * h + c < row_lo) sr[h][c] = 0xff800000u;
                     }
                 } else if (kv0 + BN - 1 > first_pos) {
 #pragma unroll
@@ -802,7 +802,7 @@ __global__ void __launch_bounds__(PrefillTcConfig<D, BS, G, NQ_, KST_, VST_>::TH
                 // l are rescaled) only when the tile's max exceeds it by more than 8, so p <= 2^8;
                 // O / l does not depend on the reference, and rescaling becomes rare, which keeps
                 // the softmax from waiting for the previous P V.
-                const float m_tile = mx * qs;
+                const float m_tile = Mod::kOn ? fmaf(mx, qs, off) : mx * qs;
                 float alpha = 1.f;
                 bool moved = false;
                 if (j == 0) {
@@ -818,7 +818,7 @@ __global__ void __launch_bounds__(PrefillTcConfig<D, BS, G, NQ_, KST_, VST_>::TH
                 // and the FMA-pipe polynomial for POLY_PAIRS of every 8 (the two units run side by
                 // side); the row sum in two packed partial sums
                 uint32_t pk[32];
-                const float2 sc2 = make_float2(qs, qs), nm2 = make_float2(-mn, -mn);
+                const float2 sc2 = make_float2(qs, qs), nm2 = Mod::kOn ? make_float2(off - mn, off - mn) : make_float2(-mn, -mn);
                 float2 rsa = make_float2(0.f, 0.f), rsb = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {

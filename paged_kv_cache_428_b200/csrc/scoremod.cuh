@@ -54,40 +54,52 @@ __device__ __forceinline__ float rcp_approx(float x)
     return y;
 }
 
-// The softmax warps of the prefill kernel are what bounds it, and their exponentials (one per score) the
-// MUFU unit.  tanh through an exponential and a reciprocal would make that three.  Scores are mostly far
-// below the cap, so where a warp's tile has |x| <= 0.6 cap throughout, tanh(y) = y q(y^2) with q of degree 4
-// that interpolates tanh(y) / y at the five Chebyshev nodes of [0, 0.36] in y^2 (absolute error below 4e-8),
-// on the FMA pipe, two scores an instruction, cap and scale inside the coefficients; else the exact form.
-#define PA_TANH_RANGE 0.6f
-#define PA_TANH_C0 0.99999992596f
-#define PA_TANH_C1 -0.33332302040f
-#define PA_TANH_C2 0.13310064426f
-#define PA_TANH_C3 -0.05209665341f
-#define PA_TANH_C4 0.01546875130f
+// The softmax warps bound the prefill kernel, and their registers are full: what is done to a score there
+// counts, and so does every branch around it.  Hence four kernels, by whether scores are capped and biased:
+//   window, prefix     only the tiles at the borders are masked; scores stay as they are.
+//   BIAS               one multiply-add to the raw score, slope / scale times the place in the tile; what the
+//                      whole tile has in common goes into the softmax's reference.  Only tiles with tokens on
+//                      both sides of a row need more.
+//   CAP                tanh(y) = y q(y^2) while a warp's tile has |x| <= 0.3 cap, q of degree 2 interpolating
+//                      tanh(y) / y at the Chebyshev nodes of [0, 0.09] in y^2 (absolute error below 4e-7), with
+//                      cap and scale inside the coefficients, on the FMA pipe; else the exact form, an
+//                      exponential and a reciprocal more for each score on the MUFU unit.
+#define PA_TANH_RANGE 0.3f
+#define PA_TANH_C0 0.99999883513f
+#define PA_TANH_C1 -0.33309988804f
+#define PA_TANH_C2 0.12633582392f
 
+template <bool CAP, bool BIAS>
 struct PrefillScoreMod {
     static constexpr bool kOn = true;
-    const float *slopes;           // [h_q] or null
+    const float *slopes;           // [h_q]
     const int32_t *prefix_lens;    // [B] or null
     int window;                    // 0: no window
     float cap_in, cap_out;         // as in ScoreModExt
     float range;                   // |raw score| up to which the polynomial holds
-    float c[5];                    // its coefficients, for raw scores and log2-domain logits
+    float c[3];                    // its coefficients, for raw scores and log2-domain logits
 
     __device__ __forceinline__ int prefix(int seq) const { return prefix_lens ? __ldg(prefix_lens + seq) : 0; }
     __device__ __forceinline__ int first_token(int pos) const { return window > 0 ? max(0, pos - window + 1) : 0; }
-    __device__ __forceinline__ float slope(int head) const
+    // What logits() leaves is to be multiplied by this: uncapped scores stay raw.
+    __device__ __forceinline__ float unit(float qk_scale) const { return CAP ? 1.f : qk_scale; }
+    // A head's slope in those units.
+    __device__ __forceinline__ float slope(int head, float qk_scale) const
     {
-        return slopes ? __ldg(slopes + head) * 1.4426950408889634f : 0.f;
+        return BIAS ? __ldg(slopes + head) * 1.4426950408889634f / unit(qk_scale) : 0.f;
     }
 
-    // Raw scores of tokens first + pos, first + pos + 1, ... of one row into log2-domain logits.
+    // Raw scores of tokens first + pos, first + pos + 1, ... of one row into logits sr + what is returned.
     // both_sides: some of the tokens may lie behind the row's position.
-    __device__ __forceinline__ void logits(uint32_t (&sr)[2][32], float qk_scale, float slope2, int first, bool both_sides) const
+    __device__ __forceinline__ float logits(uint32_t (&sr)[2][32], float slope, int first, bool both_sides) const
     {
         auto at = [&](int i) -> uint32_t & { return sr[i >> 5][i & 31]; };
-        if (cap_out > 0.f) {
+        auto pair = [&](int i) { return make_float2(__uint_as_float(at(i)), __uint_as_float(at(i + 1))); };
+        auto put = [&](int i, float2 x) {
+            at(i) = __float_as_uint(x.x);
+            at(i + 1) = __float_as_uint(x.y);
+        };
+        if constexpr (CAP) {
             float m4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < 64; i += 2)
@@ -96,15 +108,10 @@ struct PrefillScoreMod {
             if (!__any_sync(0xffffffffu, top > range)) {
 #pragma unroll
                 for (int i = 0; i < 64; i += 2) {
-                    const float2 x = make_float2(__uint_as_float(at(i)), __uint_as_float(at(i + 1)));
-                    const float2 u = __fmul2_rn(x, x);
-                    float2 q = __ffma2_rn(u, make_float2(c[4], c[4]), make_float2(c[3], c[3]));
-                    q = __ffma2_rn(u, q, make_float2(c[2], c[2]));
-                    q = __ffma2_rn(u, q, make_float2(c[1], c[1]));
+                    const float2 x = pair(i), u = __fmul2_rn(x, x);
+                    float2 q = __ffma2_rn(u, make_float2(c[2], c[2]), make_float2(c[1], c[1]));
                     q = __ffma2_rn(u, q, make_float2(c[0], c[0]));
-                    q = __fmul2_rn(x, q);
-                    at(i) = __float_as_uint(q.x);
-                    at(i + 1) = __float_as_uint(q.y);
+                    put(i, __fmul2_rn(x, q));
                 }
             } else {
 #pragma unroll
@@ -113,32 +120,19 @@ struct PrefillScoreMod {
                     at(i) = __float_as_uint(cap_out * fmaf(-2.f, rcp_approx(e + 1.f), 1.f));
                 }
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 64; i += 2) {
-                const float2 x = __fmul2_rn(make_float2(__uint_as_float(at(i)), __uint_as_float(at(i + 1))),
-                                            make_float2(qk_scale, qk_scale));
-                at(i) = __float_as_uint(x.x);
-                at(i + 1) = __float_as_uint(x.y);
-            }
         }
-        if (slopes != nullptr) {
-            const float d0 = (float)first;
-            if (both_sides) {
+        if constexpr (BIAS) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) at(i) = __float_as_uint(fmaf(slope, (float)i, __uint_as_float(at(i))));
+            if (both_sides) {                          // behind the row the bias falls again
+                const float d0 = (float)first;
 #pragma unroll
                 for (int i = 0; i < 64; ++i)
-                    at(i) = __float_as_uint(fmaf(-slope2, fabsf(d0 + (float)i), __uint_as_float(at(i))));
-            } else {
-#pragma unroll
-                for (int i = 0; i < 64; i += 2) {
-                    const float2 d = __fadd2_rn(make_float2(d0, d0), make_float2((float)i, (float)(i + 1)));
-                    const float2 x = __ffma2_rn(make_float2(slope2, slope2), d,
-                                                make_float2(__uint_as_float(at(i)), __uint_as_float(at(i + 1))));
-                    at(i) = __float_as_uint(x.x);
-                    at(i + 1) = __float_as_uint(x.y);
-                }
+                    at(i) = __float_as_uint(fmaf(-2.f * slope, fmaxf(d0 + (float)i, 0.f), __uint_as_float(at(i))));
             }
+            return slope * (float)first;
         }
+        return 0.f;
     }
 };
 

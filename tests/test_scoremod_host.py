@@ -42,7 +42,7 @@ def _prefill(**kw):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(cap=-0.5), -1), (dict(cap=NAN), -1), (dict(win=-3), -1), (dict(dt=2), -2), (dict(dt=-1), -1), (dict(scale=INF), -1),
-    (dict(mq=-1), -1), (dict(hq=6, hkv=4), -1), (dict(hq=48), -2), (dict(nb=2 ** 28), -2), (dict(qs=0), -1), (dict(q=FAKE + 8), -1),
+    (dict(scale=0.0), -1), (dict(scale=-0.1), -1), (dict(mq=-1), -1), (dict(hq=6, hkv=4), -1), (dict(hq=48), -2), (dict(nb=2 ** 28), -2), (dict(qs=0), -1), (dict(q=FAKE + 8), -1),
     (dict(ws=0), -3), (dict(wsb=255), -3), (dict(ws=FAKE + 1), -3), (dict(B=0), 0), (dict(mq=0), 0)])
 def test_prefill_refusals(kw, status):
     assert _prefill(**kw) == status
@@ -55,17 +55,20 @@ def test_workspace_goes_by_the_window():
     assert size(2, 4, 2, 64, 100, -1) == 0 and size(2, 4, 3, 64, 100) == 0
 
 
-def test_polynomial_of_tanh():
-    """tanh(y) = y q(y^2) on the range in which the kernel uses it, to 4e-8."""
+@pytest.mark.parametrize("name,rng,terms,error", [("PA_TANH_C", "PA_TANH_RANGE", 3, 4e-7)])
+def test_polynomial_of_tanh(name, rng, terms, error):
+    """tanh(y) = y q(y^2) on the range in which the kernel uses it."""
     text = (Path(__file__).resolve().parents[1] / "paged_kv_cache_428_b200" / "csrc" / "scoremod.cuh").read_text()
-    get = lambda name: float(re.search(r"#define %s (-?[0-9.]+)f" % name, text).group(1))  # noqa: E731
-    c, top = [get("PA_TANH_C%d" % i) for i in range(5)], get("PA_TANH_RANGE")
+    get = lambda what: float(re.search(r"#define %s (-?[0-9.]+)f" % what, text).group(1))  # noqa: E731
+    c, top = [get("%s%d" % (name, i)) for i in range(terms)], get(rng)
     worst = 0.0
     for i in range(20001):
         y = top * i / 20000
-        u = y * y
-        worst = max(worst, abs(y * (c[0] + u * (c[1] + u * (c[2] + u * (c[3] + u * c[4])))) - math.tanh(y)))
-    assert worst < 4e-8
+        q = 0.0
+        for a in reversed(c):
+            q = q * y * y + a
+        worst = max(worst, abs(y * q - math.tanh(y)))
+    assert worst < error
 
 
 def test_binding_refuses():
