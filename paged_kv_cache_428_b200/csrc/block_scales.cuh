@@ -315,6 +315,7 @@ __global__ void __launch_bounds__(32) copy_scales_kernel(const CopyScalesParams 
 
 // The decode: scales per block, no change of the logits.
 struct BlockScalesExt {
+    static constexpr bool kDependent = false;
     struct Args {
         const float *k_scales;     // [num_blocks][h_kv]
         const float *v_scales;

@@ -260,7 +260,7 @@ __device__ __forceinline__ SplitPlace split_locate(const int *prefix, int num_se
     return at;
 }
 
-// Ext: struct with `Args` (kernel argument), `Row<G>` (built per group; its functions for bf16 only, see
+// Ext: struct with `kDependent` (a programmatic dependent launch follows), `Args` (kernel argument), `Row<G>` (built per group; its functions for bf16 only, see
 // split_consume_bf16) and, for codes, k_scales / v_scales [num_blocks][h_kv] in Args.
 template <int D, int BS, int G, int QT, class Ext>
 __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, 5)
@@ -282,6 +282,8 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, 5)
     int *prefix = reinterpret_cast<int *>(smem + SC::OFF_PREFIX);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    // every CTA of the grid is resident at once, so a dependent grid only fills the places of CTAs that are done
+    if constexpr (Ext::kDependent) pdl_launch_dependents();
     if (threadIdx.x == 32) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(&full_bar[i], 1);

@@ -19,6 +19,7 @@ namespace pa {
 
 // ---- decode that leaves its logits ------------------------------------------------------------
 struct WeightsExt {
+    static constexpr bool kDependent = true;           // add_weights_kernel
     struct Args {
         float *logits;             // [B][h_kv][row_tokens][G]
         int row_tokens;
@@ -68,6 +69,7 @@ __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const AddWeigh
 {
     const int kvh = blockIdx.y, seq = blockIdx.z;
     const int ctx = p.context_lens[seq];
+    pdl_wait();                                        // the decode is complete
     if (ctx > p.max_tokens && blockIdx.x == 0 && kvh == 0 && threadIdx.x == 0) record_error(PA_DEVERR_BAD_LENGTH);
     const int n = min(ctx, p.max_tokens);
     const size_t row = (size_t)seq * p.h_kv + kvh;

@@ -100,8 +100,8 @@ int pa_decode_weights(void *out, float *weights, int64_t weights_stride, const v
     a.h_kv = h_kv;
     const dim3 grid((max_context_len + kAddThreads * kAddPer - 1) / (kAddThreads * kAddPer), h_kv, num_seqs);
     return switch_group(h_q / h_kv, [&](auto gc) {
-        add_weights_kernel<decltype(gc)::value><<<grid, kAddThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-        return launch_status();
+        return launch_ex(add_weights_kernel<decltype(gc)::value>, grid, dim3(kAddThreads), 0,
+                         static_cast<cudaStream_t>(stream), true, a);
     });
 }
 

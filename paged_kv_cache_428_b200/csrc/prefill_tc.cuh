@@ -805,11 +805,14 @@ __global__ void __launch_bounds__(PrefillTcConfig<D, BS, G, NQ_, KST_, VST_>::TH
                 const float m_tile = Mod::kOn ? fmaf(mx, qs, off) : mx * qs;
                 float alpha = 1.f;
                 bool moved = false;
+                // (Mod: where a bias makes later tiles' logits larger, the reference is set that much ahead)
+                float ahead = 0.f;
+                if constexpr (Mod::kOn) ahead = mod.ahead(slope * qs, pos - (kv0 + BN - 1));
                 if (j == 0) {
-                    m_run = m_tile;
+                    m_run = m_tile + ahead;
                 } else if (m_tile > m_run + 8.f) {
-                    alpha = ex2_approx(m_run - m_tile);
-                    m_run = m_tile;
+                    alpha = ex2_approx(m_run - (m_tile + ahead));
+                    m_run = m_tile + ahead;
                     moved = true;
                 }
                 // (a row that has seen no token yet, its window begins later: any finite reference gives 0)

@@ -19,6 +19,7 @@ namespace pa {
 // Bound by the bytes of K and V inside the window; 4 logits a lane and 16 tokens leave room for tanh through
 // one exponential and one division: tanh(y) = 1 - 2 / (e^2y + 1), an absolute error of about 2^-23.
 struct ScoreModExt {
+    static constexpr bool kDependent = false;
     struct Args {
         const float *slopes;       // [h_q] or null
         float cap_in, cap_out;     // 2 scale log2(e) / cap and cap log2(e); cap_out = 0: no cap
@@ -69,6 +70,13 @@ __device__ __forceinline__ float rcp_approx(float x)
 #define PA_TANH_C1 -0.33309988804f
 #define PA_TANH_C2 0.12633582392f
 
+// Places of a tile's tokens, two at a time (operands of one packed multiply-add each).
+__constant__ float2 kPlaces[32] = {
+    {0.f, 1.f}, {2.f, 3.f}, {4.f, 5.f}, {6.f, 7.f}, {8.f, 9.f}, {10.f, 11.f}, {12.f, 13.f}, {14.f, 15.f},
+    {16.f, 17.f}, {18.f, 19.f}, {20.f, 21.f}, {22.f, 23.f}, {24.f, 25.f}, {26.f, 27.f}, {28.f, 29.f}, {30.f, 31.f},
+    {32.f, 33.f}, {34.f, 35.f}, {36.f, 37.f}, {38.f, 39.f}, {40.f, 41.f}, {42.f, 43.f}, {44.f, 45.f}, {46.f, 47.f},
+    {48.f, 49.f}, {50.f, 51.f}, {52.f, 53.f}, {54.f, 55.f}, {56.f, 57.f}, {58.f, 59.f}, {60.f, 61.f}, {62.f, 63.f}};
+
 template <bool CAP, bool BIAS>
 struct PrefillScoreMod {
     static constexpr bool kOn = true;
@@ -87,6 +95,15 @@ struct PrefillScoreMod {
     __device__ __forceinline__ float slope(int head, float qk_scale) const
     {
         return BIAS ? __ldg(slopes + head) * 1.4426950408889634f / unit(qk_scale) : 0.f;
+    }
+
+    // What the bias can still add to the largest logit of a tile whose last token lies `distance` before the row:
+    // with the reference that far ahead O is rarely rescaled on the way to the row's own position (a steep
+    // head gains 46 for every tile).  At most 96, so that what the reference turns out to be too far ahead
+    // costs nothing: probabilities of 2^-96 are as exact as those of 1.
+    __device__ __forceinline__ float ahead(float slope_log2, int distance) const
+    {
+        return BIAS ? fminf(96.f, fmaxf(0.f, slope_log2 * (float)distance)) : 0.f;
     }
 
     // Raw scores of tokens first + pos, first + pos + 1, ... of one row into logits sr + what is returned.
@@ -122,8 +139,9 @@ struct PrefillScoreMod {
             }
         }
         if constexpr (BIAS) {
+            const float2 s2 = make_float2(slope, slope);
 #pragma unroll
-            for (int i = 0; i < 64; ++i) at(i) = __float_as_uint(fmaf(slope, (float)i, __uint_as_float(at(i))));
+            for (int i = 0; i < 64; i += 2) put(i, __ffma2_rn(s2, kPlaces[i / 2], pair(i)));
             if (both_sides) {                          // behind the row the bias falls again
                 const float d0 = (float)first;
 #pragma unroll
