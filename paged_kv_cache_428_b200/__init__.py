@@ -465,6 +465,8 @@ def _on_current_device(stream, *tensors) -> int:
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError("tensor on %s, but the current device is cuda:%d" % (t.device, dev))
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)      # torch.cuda.current_stream(), without its object
     if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
         raise ValueError("stream of cuda:%d, but the current device is cuda:%d" % (stream.device_index, dev))
     return _stream_ptr(stream)
@@ -473,13 +475,11 @@ def _on_current_device(stream, *tensors) -> int:
 QUANT_DTYPES = (torch.uint8, torch.float8_e4m3fn, torch.int8)
 
 
-def _need_block_scales(k_cache, v_cache, k_scales, v_scales) -> None:
-    _need(k_cache, "k_cache", QUANT_DTYPES, 4)
-    _need(v_cache, "v_cache", (k_cache.dtype,), 4)
+def _need_scales(k_scales, v_scales, num_blocks: int, h_kv: int) -> None:
     _need(k_scales, "k_scales", (torch.float32,), 2)
     _need(v_scales, "v_scales", (torch.float32,), 2)
-    if v_cache.shape != k_cache.shape or tuple(k_scales.shape) != tuple(k_cache.shape[:2]) or v_scales.shape != k_scales.shape:
-        raise ValueError("shape mismatch between caches and block scales (scales are [num_blocks, h_kv])")
+    if k_scales.shape != (num_blocks, h_kv) or v_scales.shape != (num_blocks, h_kv):
+        raise ValueError("block scales must be [num_blocks, h_kv] = [%d, %d]" % (num_blocks, h_kv))
 
 
 def make_block_scales(num_blocks: int, h_kv: int, device="cuda") -> tuple:
@@ -491,8 +491,10 @@ def pa_reshape_and_cache_block_scales(key, value, k_cache, v_cache, k_scales, v_
                                       stream=None) -> None:
     """Write bf16 rows [T, h_kv, d] into 8-bit caches with one scale for each (block, KV head); the scales
     are kept by the call.  The tokens of one block stand next to each other in slot_mapping."""
-    _need_block_scales(k_cache, v_cache, k_scales, v_scales)
+    if k_cache.dtype not in QUANT_DTYPES:
+        raise TypeError("k_cache: dtype %s, expected one of %s" % (k_cache.dtype, QUANT_DTYPES))
     r = reshape_call_args(key, value, k_cache, v_cache, slot_mapping)
+    _need_scales(k_scales, v_scales, r[11], r[8])
     _check(_lib.pa_reshape_and_cache_block_scales(
         *r[:6], k_scales.data_ptr(), v_scales.data_ptr(), *r[6:13],
         _on_current_device(stream, key, value, k_cache, v_cache, k_scales, v_scales, slot_mapping)),
@@ -539,26 +541,27 @@ def _split_workspace(workspace, size: int, device) -> torch.Tensor:
     return workspace
 
 
-def _need_decode(out, q, k_cache, v_cache, block_tables, context_lens, dtypes) -> None:
+def _need_decode(out, q, k_cache, v_cache, block_tables, context_lens, dtypes) -> tuple:
+    """Checks of the split decodes; (num_seqs, h_q, head_dim, num_blocks, h_kv, block_size)."""
     _need(out, "out", (torch.bfloat16,), 3)
     _need(q, "q", (torch.bfloat16,), 3)
     _need(k_cache, "k_cache", dtypes, 4)
     _need(v_cache, "v_cache", (k_cache.dtype,), 4)
     _need(block_tables, "block_tables", (torch.int32,), 2)
     _need(context_lens, "context_lens", (torch.int32,), 1)
-    if out.shape != q.shape or k_cache.shape[3] != q.shape[2] or v_cache.shape != k_cache.shape \
-            or block_tables.shape[0] != q.shape[0] or context_lens.shape[0] != q.shape[0]:
+    size, pool = q.shape, k_cache.shape
+    if out.shape != size or pool[3] != size[2] or v_cache.shape != pool or block_tables.shape[0] != size[0] \
+            or context_lens.shape[0] != size[0]:
         raise ValueError("shape mismatch between out, q, caches, block_tables and context_lens")
+    return *size, *pool[:3]
 
 
 def pa_decode_block_scales(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
                            max_context_len: int, scale: float = None, workspace: Optional[torch.Tensor] = None,
                            stream=None) -> torch.Tensor:
     """pa_decode over an 8-bit cache with one scale for each (block, KV head); returns out."""
-    _need_decode(out, q, k_cache, v_cache, block_tables, context_lens, QUANT_DTYPES)
-    _need_block_scales(k_cache, v_cache, k_scales, v_scales)
-    B, h_q, d = q.shape
-    NB, h_kv, bs, _ = k_cache.shape
+    B, h_q, d, NB, h_kv, bs = _need_decode(out, q, k_cache, v_cache, block_tables, context_lens, QUANT_DTYPES)
+    _need_scales(k_scales, v_scales, NB, h_kv)
     ws = _split_workspace(workspace, 0 if workspace is not None else pa_decode_block_scales_workspace_size(
         B, h_q, h_kv, d, max_context_len), q.device)
     _check(_lib.pa_decode_block_scales(
@@ -590,9 +593,7 @@ def pa_decode_scoremod(out, q, k_cache, v_cache, block_tables, context_lens, max
                        workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """pa_decode with scores capped by softcap * tanh(x / softcap), less alibi_slopes[h] times the distance, over
     the last `window` tokens; each is off by default.  Returns out."""
-    _need_decode(out, q, k_cache, v_cache, block_tables, context_lens, CACHE_DTYPES)
-    B, h_q, d = q.shape
-    NB, h_kv, bs, _ = k_cache.shape
+    B, h_q, d, NB, h_kv, bs = _need_decode(out, q, k_cache, v_cache, block_tables, context_lens, CACHE_DTYPES)
     ws = _split_workspace(workspace, 0 if workspace is not None else pa_decode_scoremod_workspace_size(
         B, h_q, h_kv, d, max_context_len, window), q.device)
     _check(_lib.pa_decode_scoremod(
@@ -634,10 +635,8 @@ def pa_decode_weights(out, weights, q, k_cache, v_cache, block_tables, context_l
                       scale: float = None, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """pa_decode that also adds each cached token's softmax weights, summed over the query heads of its KV head,
     to weights fp32 [B, h_kv, >= max_context_len]; returns out."""
-    _need_decode(out, q, k_cache, v_cache, block_tables, context_lens, CACHE_DTYPES)
+    B, h_q, d, NB, h_kv, bs = _need_decode(out, q, k_cache, v_cache, block_tables, context_lens, CACHE_DTYPES)
     _need(weights, "weights", (torch.float32,), 3)
-    B, h_q, d = q.shape
-    NB, h_kv, bs, _ = k_cache.shape
     if weights.shape[0] != B or weights.shape[1] != h_kv:
         raise ValueError("weights must be [%d, %d, n], got %s" % (B, h_kv, tuple(weights.shape)))
     ws = _split_workspace(workspace, 0 if workspace is not None else pa_decode_weights_workspace_size(

@@ -18,7 +18,7 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 OBJ = PKG / "_build"
 LIB = PKG / "libpa.so"
-SOURCES = [CSRC / f for f in ("pa_lib.cu", "pa_block_scales.cu", "pa_evict.cu", "pa_scoremod.cu", "host.cpp", "allocator.cpp")]
+SOURCES = [CSRC / f for f in ("pa_lib.cu", "pa_block_scales.cu", "pa_evict.cu", "pa_scoremod.cu", "pa_prefill_scoremod.cu", "host.cpp", "allocator.cpp")]
 HEADERS = [ROOT / "include" / "pa.h"] + sorted(CSRC.glob("*.cuh"))
 
 NVCC_FLAGS = [

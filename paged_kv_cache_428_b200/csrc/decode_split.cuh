@@ -8,13 +8,14 @@
 // Schedule.  The step's work is the list of all (sequence, KV head, block) triples in that order.  With
 // C CTAs (as many as the GPU holds at once, fewer for small steps) CTA c takes the triples
 // [c u, (c + 1) u), u = ceil(T / C): every CTA moves the same number of blocks, so they end together
-// whatever the lengths are.  u is at least kSplitMinTokens tokens (a shorter range would cost more
-// in merging than it saves) and at least 1/62 of the longest sequence, so that at most
-// kSplitMaxPieces CTAs share one (sequence, KV head) group.  The lengths are read on the device; the
-// host's bound on them only sizes the grid.
+// whatever the lengths are.  u is at least kSplitMinTokens tokens (a shorter range costs more in merging
+// than it saves) and at least 1/62 of the longest sequence, so that at most kSplitMaxPieces CTAs share one
+// (sequence, KV head) group.  Where the CTAs suffice for it, no range crosses the border of a group: each
+// group is cut into ceil(blocks / u) even pieces, short sequences need no merge, and no CTA ends two groups.  The
+// lengths are read on the device; the host's bound on them only sizes the grid.
 //   A producer warp streams the blocks' K and V tiles by 2-D TMA through an mbarrier ring, without a
 // pause between groups: lane j looks up triple j of the next 32 (and its scales) while the present 32
-// are issued.  Two consumer warps take alternate blocks (mma.sync m16n8k16, tokens or head dims on
+// are issued.  Consumer warps take blocks in turn (mma.sync m16n8k16, tokens or head dims on
 // the 16 rows, the group's query heads on the 8 columns, as in decode_mma.cuh and decode_q8.cuh) and put
 // their states together where a group or the CTA's range ends.  A group that lies in one range is
 // finished there.  Otherwise each CTA leaves (m, l, o) in one of its two slots (0: the group its range
@@ -33,7 +34,7 @@ namespace pa {
 constexpr int kSplitMaxSeqs = 4096;       // sequences of one launch (block prefix sums in shared memory)
 constexpr int kSplitMaxCtas = 1024;       // partial slots in the workspace: two for each of this many CTAs
 constexpr int kSplitMaxPieces = 64;       // CTAs that share one group
-constexpr int kSplitMinTokens = 64;       // tokens of the shortest range of one CTA
+constexpr int kSplitMinTokens = 128;      // tokens of the shortest range of one CTA
 constexpr int kSplitMaxGroups = 65536;    // (sequence, KV head) groups of one call: counters at the workspace's front
 
 struct SplitParams {
@@ -65,22 +66,35 @@ struct SplitStage {
 
 template <int D, int BS, int G, int QT>
 struct SplitConfig {
-    using Tile = std::conditional_t<QT == 0, MmaDecodeConfig<D, BS, G>, MmaQ8Config<D, BS, G>>;
+    // Consumer warps, ring, CTAs of an SM.  One producer warp feeds its consumers only so fast (with a lane a
+    // block and one block at a time, E4M3 at 32 x 4096 tokens x 32 heads: 198 us at 5 x 2 consumers, 213 at 4 x 3, 328
+    // at 2 x 7; with half the ring at a time 199, 187 and 189 at 5 x 2, 4 x 3 and 3 x 4).  bf16, 64 sequences: 102.9
+    // to 107.2 us over the same range, 103.2 at 3 x 4, where single groups are also done soonest.
+    static constexpr int kWarps = QT != 0 ? 3 : BS * D >= 64 * 128 ? 2 : 4;
+    static constexpr int kRing = QT != 0 ? 49152 : 65536, kPerSm = QT != 0 ? 4 : 3;
+    using Tile = std::conditional_t<QT == 0, MmaDecodeConfig<D, BS, G, kWarps, kRing>, MmaQ8Config<D, BS, G, kWarps, kRing>>;
     static constexpr int NW = Tile::NW;
     static constexpr int THREADS = Tile::THREADS;
     static constexpr int STAGES = Tile::STAGES;
+    // blocks that the producer issues together, a lane each: half the ring (a power of two)
+    static constexpr int kIssue = STAGES >= 64 ? 32 : STAGES >= 32 ? 16 : STAGES >= 16 ? 8 : STAGES >= 8 ? 4 : STAGES >= 4 ? 2 : 1;
     static constexpr int OFF_BARS = Tile::RING;
     static constexpr int OFF_STAGE = OFF_BARS + 2 * STAGES * 8;
-    static constexpr int OFF_FLAGS = OFF_STAGE + STAGES * (int)sizeof(SplitStage);   // abort, last, longest, bad[2]
-    static constexpr int OFF_COMBINE = OFF_FLAGS + 32;
-    static constexpr int OFF_MERGE = OFF_COMBINE + NW * G * (D + 2) * 4;             // [2][G][kSplitMaxPieces]
-    static constexpr int OFF_PREFIX = OFF_MERGE + 2 * G * kSplitMaxPieces * 4;
-    static constexpr int smem_bytes(int num_seqs) { return OFF_PREFIX + (num_seqs + 1) * 4 + 1024; }
+    static constexpr int OFF_FLAGS = OFF_STAGE + STAGES * (int)sizeof(SplitStage);   // abort, last, longest, bad[NW]
+    static constexpr int OFF_COMBINE = OFF_FLAGS + 48;
+    static constexpr int OFF_MERGE = OFF_COMBINE + NW * G * (D + 2) * 4;             // [G][kSplitMaxPieces]
+    static constexpr int OFF_PREFIX = OFF_MERGE + G * kSplitMaxPieces * 4;
+    static constexpr int smem_bytes(int num_seqs) { return OFF_PREFIX + 2 * (num_seqs + 1) * 4 + 1024; }
     static_assert(Tile::RING % 16 == 0 && OFF_STAGE % 16 == 0 && OFF_COMBINE % 16 == 0, "alignment");
-    static_assert(NW == 2, "two consumer warps");
+    static_assert(3 + NW <= 12, "flags");
+    static_assert(kSplitMaxPieces == 64, "two pieces a lane");
 };
 
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 64;" ::: "memory"); }
+template <int NW>
+__device__ __forceinline__ void consumers_sync()
+{
+    asm volatile("bar.sync 1, %0;" ::"n"(NW * 32) : "memory");
+}
 
 // What a consumer warp keeps of a group: running maximum and sum for heads 2 (lane % 4) and + 1, and
 // the unnormalised output in the accumulator layout of the tile's consume function.
@@ -156,16 +170,18 @@ __device__ __forceinline__ void split_consume_bf16(uint8_t *ktile, int lo, int h
     for (int sub = 0; sub < C::NSUB; ++sub) {
         if (sub * 16 >= hi) break;
         if (sub * 16 + 16 <= lo) continue;
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, odd[4] = {0.f, 0.f, 0.f, 0.f};      // two chains of half the length
         {
             const int tok = sub * 16 + (mat & 1) * 8 + mrow;
 #pragma unroll
             for (int ks = 0; ks < C::KS; ++ks) {
                 uint32_t a[4];
                 ldmatrix_x4(a, kbase + (ks >> 2) * C::HALF_BYTES + swz128(tok, 2 * (ks & 3) + (mat >> 1)));
-                mma_bf16_16816(s, a[0], a[1], a[2], a[3], qb[ks][0], qb[ks][1]);
+                mma_bf16_16816(ks & 1 ? odd : s, a[0], a[1], a[2], a[3], qb[ks][0], qb[ks][1]);
             }
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] += odd[i];
         const int t0 = sub * 16 + r;
         const bool use0 = t0 >= lo && t0 < hi, use1 = t0 + 8 >= lo && t0 + 8 < hi;
         float x[4], p[4];
@@ -263,7 +279,7 @@ __device__ __forceinline__ SplitPlace split_locate(const int *prefix, int num_se
 // Ext: struct with `kDependent` (a programmatic dependent launch follows), `Args` (kernel argument), `Row<G>` (built per group; its functions for bf16 only, see
 // split_consume_bf16) and, for codes, k_scales / v_scales [num_blocks][h_kv] in Args.
 template <int D, int BS, int G, int QT, class Ext>
-__global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, 5)
+__global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, SplitConfig<D, BS, G, QT>::kPerSm)
     paged_decode_split_kernel(const SplitParams p, const typename Ext::Args args,
                               const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v)
 {
@@ -279,7 +295,7 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, 5)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SC::OFF_FLAGS);
     volatile int *last_flag = abort_flag + 1, *bad_flag = abort_flag + 3;       // bad_flag: one for each consumer warp
     int *longest = const_cast<int *>(abort_flag + 2);
-    int *prefix = reinterpret_cast<int *>(smem + SC::OFF_PREFIX);
+    int *prefix = reinterpret_cast<int *>(smem + SC::OFF_PREFIX), *cuts = prefix + p.num_seqs + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // every CTA of the grid is resident at once, so a dependent grid only fills the places of CTAs that are done
@@ -312,10 +328,27 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, 5)
             carry += __shfl_sync(FULL, sum, 31);
         }
         most = __reduce_max_sync(FULL, most);
+        __syncwarp();
         if (lane == 0) {
             prefix[p.num_seqs] = carry;
             *longest = most;
         }
+        __syncwarp();
+        // cuts[s] = pieces of one KV head of the sequences before s, at the smallest u
+        const int u_min = max(kSplitMinTokens / BS, ceil_div(most, kSplitMaxPieces - 2));
+        carry = 0;
+        for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
+            const int s = s0 + lane, n = s < p.num_seqs ? ceil_div(prefix[s + 1] - prefix[s], u_min) : 0;
+            int sum = n;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int y = __shfl_up_sync(FULL, sum, off);
+                if (lane >= off) sum += y;
+            }
+            if (s < p.num_seqs) cuts[s] = carry + sum - n;
+            carry += __shfl_sync(FULL, sum, 31);
+        }
+        if (lane == 0) cuts[p.num_seqs] = carry;
     }
     __syncthreads();
     // sequences without a token: zero rows
@@ -325,9 +358,26 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, 5)
                 reinterpret_cast<uint4 *>(p.out + (size_t)s * p.h_q * D)[i] = make_uint4(0, 0, 0, 0);
 
     const long long total = (long long)prefix[p.num_seqs] * p.h_kv;
-    long long u = (total + gridDim.x - 1) / gridDim.x;
-    u = max(u, (long long)max(kSplitMinTokens / BS, ceil_div(*longest, kSplitMaxPieces - 2)));
-    const long long x0 = (long long)blockIdx.x * u, x1 = min(total, x0 + u);
+    const int u_min = max(kSplitMinTokens / BS, ceil_div(*longest, kSplitMaxPieces - 2));
+    // pieces of u_min blocks at most, whole groups: this CTA's sequence and piece, if there are CTAs enough
+    const bool aligned = (long long)cuts[p.num_seqs] * p.h_kv <= gridDim.x;
+    long long u = 0, x0 = 0, x1 = 0;
+    int first_cta = 0, group_pieces = 0;                       // aligned: of this CTA's group
+    if (aligned) {
+        if ((int)blockIdx.x < cuts[p.num_seqs] * p.h_kv) {
+            const SplitPlace at = split_locate(cuts, p.num_seqs, p.h_kv, blockIdx.x);    // at.nb, at.block: pieces
+            const int nb = prefix[at.seq + 1] - prefix[at.seq], each = ceil_div(nb, at.nb);
+            const long long group0 = (long long)prefix[at.seq] * p.h_kv + (long long)at.kvh * nb;
+            first_cta = (int)blockIdx.x - at.block;
+            group_pieces = ceil_div(nb, each);
+            x0 = group0 + min(nb, at.block * each);
+            x1 = group0 + min(nb, (at.block + 1) * each);
+        }
+    } else {
+        u = max((total + gridDim.x - 1) / gridDim.x, (long long)u_min);
+        x0 = (long long)blockIdx.x * u;
+        x1 = min(total, x0 + u);
+    }
     if (x0 >= x1) return;                                      // uniform over the CTA
 
     if (warp == NW) {
@@ -369,40 +419,43 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, 5)
                 v_inv = 1.f / v;
             }
             const int cnt = min(32, n - i0);
-            for (int j = 0; j < cnt; ++j) {
-                const int r = __shfl_sync(FULL, row, j), i = i0 + j, st = i % STAGES;
-                const float k_j = __shfl_sync(FULL, ks, j), l_j = __shfl_sync(FULL, v_log2, j), v_j = __shfl_sync(FULL, v_inv, j);
-                if (lane == 0) {
-                    if (i >= STAGES) ok = mbar_wait_bounded(&empty_bar[st], ((i / STAGES) - 1) & 1);
-                    if (ok && *abort_flag) ok = false;
-                    if (ok) {
-                        stage[st].bad = r < 0;
-                        stage[st].k_scale = k_j;
-                        stage[st].v_log2 = l_j;
-                        stage[st].v_inv = v_j;
-                        if (r >= 0) {
-                            mbar_arrive_expect_tx(&full_bar[st], C::STAGE_BYTES);
-                            uint8_t *dst = smem + st * C::STAGE_BYTES;
-                            if constexpr (QT == 0) {
+            for (int j0 = 0; j0 < cnt && ok; j0 += SC::kIssue) {
+                const bool mine = lane >= j0 && lane < min(j0 + SC::kIssue, cnt);
+                const int i = i0 + lane, st = i % STAGES;
+                bool free = true;
+                if (mine) {
+                    if (i >= STAGES) free = mbar_wait_bounded(&empty_bar[st], ((i / STAGES) - 1) & 1);
+                    free = free && !*abort_flag;
+                }
+                ok = __all_sync(FULL, free);
+                if (!ok) break;
+                if (mine) {
+                    stage[st].bad = row < 0;
+                    if constexpr (QT != 0) {
+                        stage[st].k_scale = ks;
+                        stage[st].v_log2 = v_log2;
+                        stage[st].v_inv = v_inv;
+                    }
+                    if (row >= 0) {
+                        mbar_arrive_expect_tx(&full_bar[st], C::STAGE_BYTES);
+                        uint8_t *dst = smem + st * C::STAGE_BYTES;
+                        if constexpr (QT == 0) {
 #pragma unroll
-                                for (int hf = 0; hf < C::HALVES; ++hf) {
-                                    tma_load_2d(dst + hf * C::HALF_BYTES, &tmap_k, hf * 64, r, &full_bar[st], pol);
-                                    tma_load_2d(dst + C::TILE + hf * C::HALF_BYTES, &tmap_v, hf * 64, r, &full_bar[st],
-                                                pol);
-                                }
-                            } else {
-                                tma_load_2d(dst, &tmap_k, 0, r, &full_bar[st], pol);
-                                tma_load_2d(dst + C::TILE, &tmap_v, 0, r, &full_bar[st], pol);
+                            for (int hf = 0; hf < C::HALVES; ++hf) {
+                                tma_load_2d(dst + hf * C::HALF_BYTES, &tmap_k, hf * 64, row, &full_bar[st], pol);
+                                tma_load_2d(dst + C::TILE + hf * C::HALF_BYTES, &tmap_v, hf * 64, row, &full_bar[st], pol);
                             }
                         } else {
-                            record_error(PA_DEVERR_BAD_BLOCK);
-                            mbar_arrive(&full_bar[st]);
+                            tma_load_2d(dst, &tmap_k, 0, row, &full_bar[st], pol);
+                            tma_load_2d(dst + C::TILE, &tmap_v, 0, row, &full_bar[st], pol);
                         }
-                        issued = i + 1;
+                    } else {
+                        record_error(PA_DEVERR_BAD_BLOCK);
+                        mbar_arrive(&full_bar[st]);
                     }
                 }
-                ok = __shfl_sync(FULL, ok, 0) != 0;
-                if (!ok) break;
+                __syncwarp();
+                issued = i0 + min(j0 + SC::kIssue, cnt);
             }
         }
         if (lane == 0) {
@@ -418,10 +471,10 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, 5)
     }
 
     // ------------------------------ consumers ------------------------------
-    float *cm = reinterpret_cast<float *>(smem + SC::OFF_COMBINE);           // [NW][G]
+    float *co = reinterpret_cast<float *>(smem + SC::OFF_COMBINE);           // [NW][G][D], read 16 bytes at a time
+    float *cm = co + NW * G * D;                                             // [NW][G]
     float *cl = cm + NW * G;                                                 // [NW][G]
-    float *co = cl + NW * G;                                                 // [NW][G][D]
-    float *mw = reinterpret_cast<float *>(smem + SC::OFF_MERGE), *lw = mw + G * kSplitMaxPieces;
+    float *mw = reinterpret_cast<float *>(smem + SC::OFF_MERGE);             // [G][kSplitMaxPieces]
     const int tid = threadIdx.x, tq = lane & 3, r8 = lane >> 2;
     int k0 = 0;                                                              // ring index of the group's first block
     for (long long x = x0; x < x1;) {
@@ -444,7 +497,7 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, 5)
         state.clear();
         const typename Ext::template Row<G> row(args, p, at.seq, at.kvh, ctx, lane);
         bool bad = false;
-        for (int i = (warp - k0) & (NW - 1); i < n; i += NW) {
+        for (int i = (warp + NW - k0 % NW) % NW; i < n; i += NW) {
             if (*abort_flag) break;
             const int k = k0 + i, st = k % STAGES;
             if (!__all_sync(FULL, mbar_wait_bounded(&full_bar[st], (k / STAGES) & 1))) {
@@ -476,7 +529,7 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, 5)
         k0 += n;
         x += n;
 
-        // ---- the two warps' states of this group ----
+        // ---- the warps' states of this group ----
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
             state.l[0] += __shfl_xor_sync(FULL, state.l[0], off);
@@ -504,20 +557,27 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, 5)
                 }
             }
         }
-        consumers_sync();
-        const bool failed = *abort_flag != 0 || bad_flag[0] != 0 || bad_flag[1] != 0;
+        consumers_sync<NW>();
+        bool failed = *abort_flag != 0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) failed = failed || bad_flag[w] != 0;
         const bool whole = at.block == 0 && n == at.nb;
         const long long group0 = x - n - at.block;                           // the group's first triple
-        const int slot = 2 * blockIdx.x + (group0 > x0 ? 1 : 0);
+        const int slot = 2 * blockIdx.x + (!aligned && group0 > x0 ? 1 : 0);
         const float nan = __int_as_float(0x7fc00000);
         for (int idx = tid; idx < G * D / 4; idx += NW * 32) {
             const int h = idx / (D / 4), d4 = idx % (D / 4);
-            const float M = fmaxf(cm[h], cm[G + h]);
-            const float w0 = cm[h] == M ? 1.f : exp2f(cm[h] - M), w1 = cm[G + h] == M ? 1.f : exp2f(cm[G + h] - M);
-            const float L = cl[h] * w0 + cl[G + h] * w1;
-            const float4 a = reinterpret_cast<const float4 *>(co + h * D)[d4];
-            const float4 b = reinterpret_cast<const float4 *>(co + (G + h) * D)[d4];
-            float4 o = make_float4(a.x * w0 + b.x * w1, a.y * w0 + b.y * w1, a.z * w0 + b.z * w1, a.w * w0 + b.w * w1);
+            float M = cm[h], L = 0.f;
+#pragma unroll
+            for (int w = 1; w < NW; ++w) M = fmaxf(M, cm[w * G + h]);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float f = cm[w * G + h] == M ? 1.f : exp2f(cm[w * G + h] - M);
+                const float4 a = reinterpret_cast<const float4 *>(co + (w * G + h) * D)[d4];
+                L += cl[w * G + h] * f;
+                o = make_float4(fmaf(a.x, f, o.x), fmaf(a.y, f, o.y), fmaf(a.z, f, o.z), fmaf(a.w, f, o.w));
+            }
             if (whole) {
                 const float inv = failed ? nan : (L == 0.f ? 0.f : 1.f / L);
                 *reinterpret_cast<uint2 *>(p.out + (head0 + h) * D + 4 * d4) =
@@ -529,13 +589,14 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, 5)
                 if (d4 == 0) reinterpret_cast<float2 *>(p.part_ml)[(size_t)slot * G + h] = make_float2(M, failed ? nan : L);
             }
         }
-        consumers_sync();                                                    // states read, partials written
+        consumers_sync<NW>();                                                    // states read, partials written
         if (whole) continue;
 
         // ---- count; the CTA that completes the group merges it ----
         // the barrier orders all partial writes before thread 0's fence and count (release); whoever sees
         // the count complete fences before its threads read the others' partials (acquire)
-        const int c0 = (int)(group0 / u), c1 = (int)((group0 + at.nb - 1) / u), pieces = c1 - c0 + 1;
+        const int c0 = aligned ? first_cta : (int)(group0 / u);
+        const int pieces = aligned ? group_pieces : (int)((group0 + at.nb - 1) / u) - c0 + 1;
         if (tid == 0) {
             int *cnt = p.counters + (size_t)at.seq * p.h_kv + at.kvh;
             __threadfence();
@@ -546,31 +607,31 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, 5)
             }
             *last_flag = is_last;
         }
-        consumers_sync();
+        consumers_sync<NW>();
         if (!*last_flag) continue;
-        auto slot_of = [&](int c) { return 2 * c + (group0 > (long long)c * u ? 1 : 0); };
-        for (int idx = tid; idx < G * pieces; idx += NW * 32) {
-            const int h = idx / pieces, c = idx % pieces;
-            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml) + (size_t)slot_of(c0 + c) * G + h);
-            mw[h * kSplitMaxPieces + c] = ml.x;
-            lw[h * kSplitMaxPieces + c] = ml.y;
-        }
-        consumers_sync();
-        if (tid < G) {
-            float *m = mw + tid * kSplitMaxPieces;
-            const float *l = lw + tid * kSplitMaxPieces;
-            float M = -INFINITY, L = 0.f;
-            for (int c = 0; c < pieces; ++c) M = fmaxf(M, m[c]);
-            for (int c = 0; c < pieces; ++c) {
-                const float w = m[c] == M ? 1.f : exp2f(m[c] - M);
-                m[c] = w;
-                L += w * l[c];
+        auto slot_of = [&](int c) { return 2 * c + (!aligned && group0 > (long long)c * u ? 1 : 0); };
+        // a warp for each head, a lane for each piece (and the one 32 further): weights 2^(m - M) / L
+        for (int h = warp; h < G; h += NW) {
+            float2 ml[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int c = lane + 32 * i;
+                ml[i] = c < pieces ? __ldcg(reinterpret_cast<const float2 *>(p.part_ml) + (size_t)slot_of(c0 + c) * G + h)
+                                   : make_float2(-INFINITY, 0.f);
             }
+            float M = fmaxf(ml[0].x, ml[1].x);
+#pragma unroll
+            for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, off));
+            const float w0 = ml[0].x == M ? 1.f : exp2f(ml[0].x - M), w1 = ml[1].x == M ? 1.f : exp2f(ml[1].x - M);
+            float L = w0 * ml[0].y + w1 * ml[1].y;
+#pragma unroll
+            for (int off = 16; off >= 1; off >>= 1) L += __shfl_xor_sync(FULL, L, off);
             const float inv = L == 0.f ? 0.f : 1.f / L;
-            for (int c = 0; c < pieces; ++c) m[c] *= inv;
-            if (p.lse) p.lse[head0 + tid] = log2_sum(M, L);
+            mw[h * kSplitMaxPieces + lane] = w0 * inv;
+            mw[h * kSplitMaxPieces + lane + 32] = w1 * inv;
+            if (lane == 0 && p.lse) p.lse[head0 + h] = log2_sum(M, L);
         }
-        consumers_sync();
+        consumers_sync<NW>();
         for (int idx = tid; idx < G * D / 4; idx += NW * 32) {
             const int h = idx / (D / 4), d4 = idx % (D / 4);
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -594,7 +655,7 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, 5)
             *reinterpret_cast<uint2 *>(p.out + (head0 + h) * D + 4 * d4) =
                 make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
         }
-        consumers_sync();                                                    // mw / last_flag free for the next group
+        consumers_sync<NW>();                                                    // mw / last_flag free for the next group
     }
 }
 

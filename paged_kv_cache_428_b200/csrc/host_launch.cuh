@@ -215,10 +215,14 @@ int collect_device_errors(unsigned int *flags, int clear)
     return PA_OK;
 }
 
+// tanh cap of the scores: 0 = none.
+bool valid_softcap(float cap) { return std::isfinite(cap) && cap >= 0.f; }
+
 }  // namespace
 
 int block_scales_errors(unsigned int *flags, int clear);    // pa_block_scales.cu
 int evict_errors(unsigned int *flags, int clear);           // pa_evict.cu
 int scoremod_errors(unsigned int *flags, int clear);        // pa_scoremod.cu
+int prefill_scoremod_errors(unsigned int *flags, int clear);    // pa_prefill_scoremod.cu
 
 }  // namespace pa

@@ -961,6 +961,7 @@ int pa_device_errors(unsigned int *flags, int clear)
     if (rc == PA_OK) rc = block_scales_errors(&v, clear);
     if (rc == PA_OK) rc = evict_errors(&v, clear);
     if (rc == PA_OK) rc = scoremod_errors(&v, clear);
+    if (rc == PA_OK) rc = prefill_scoremod_errors(&v, clear);
     if (rc != PA_OK) return rc;
     *flags = v;
     return PA_OK;

@@ -55,7 +55,7 @@
 //              every S product that read the Q tiles has finished.
 // Modified scores.  `Mod` changes what a score becomes and which tokens a row sees; every difference
 // stands under `if constexpr (Mod::kOn)`, and PrefillPlain is the kernel without any (see
-// scoremod_prefill.cuh for the other one).
+// scoremod_prefill.cuh for the others).
 // Every wait on the data path is bounded and also ends when another role has stopped the CTA; on
 // a timeout or a bad block the CTA records the error, stops claiming, writes NaN into the rows
 // of the items it holds, waits for its copies and MMAs in flight and frees its tensor memory.

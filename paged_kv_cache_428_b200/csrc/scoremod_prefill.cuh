@@ -1,5 +1,5 @@
-// scoremod.cuh -- attention with modified scores, for single tokens (on decode_split.cuh) and for chunks (on
-// prefill_tc.cuh).  With p the position of the query and t that of the key:
+// scoremod_prefill.cuh -- chunked-prefill attention with modified scores, on prefill_tc.cuh.  With p the position
+// of the query and t that of the key:
 //
 //   x = scale q . k                              the score
 //   x = cap tanh(x / cap)                        softcap > 0
@@ -10,44 +10,10 @@
 // The logits are kept in the log2 domain (times log2 e) like all scores of this library.
 #pragma once
 
-#include "decode_split.cuh"
 #include "prefill_tc.cuh"
 
 namespace pa {
 
-// ---- single tokens ----------------------------------------------------------------------------
-// Bound by the bytes of K and V inside the window; 4 logits a lane and 16 tokens leave room for tanh through
-// one exponential and one division: tanh(y) = 1 - 2 / (e^2y + 1), an absolute error of about 2^-23.
-struct ScoreModExt {
-    static constexpr bool kDependent = false;
-    struct Args {
-        const float *slopes;       // [h_q] or null
-        float cap_in, cap_out;     // 2 scale log2(e) / cap and cap log2(e); cap_out = 0: no cap
-    };
-    template <int G>
-    struct Row {
-        float scale, cap_in, cap_out, slope[2];
-        int last;
-        __device__ __forceinline__ Row(const Args &a, const SplitParams &p, int, int kvh, int ctx, int lane)
-            : scale(p.qk_scale), cap_in(a.cap_in), cap_out(a.cap_out), last(ctx - 1)
-        {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int h = 2 * (lane & 3) + j;
-                slope[j] = a.slopes != nullptr && h < G ? __ldg(a.slopes + kvh * G + h) * 1.4426950408889634f : 0.f;
-            }
-        }
-        __device__ __forceinline__ float logit(float dot, int t, int j) const
-        {
-            float x = dot * scale;
-            if (cap_out > 0.f) x = cap_out * (1.f - __fdividef(2.f, exp2f(dot * cap_in) + 1.f));
-            return fmaf(slope[j], (float)(t - last), x);
-        }
-        __device__ __forceinline__ void keep(const float (&)[4], int, bool, bool) const {}
-    };
-};
-
-// ---- chunks -----------------------------------------------------------------------------------------
 __device__ __forceinline__ float rcp_approx(float x)
 {
     float y;
@@ -83,7 +49,7 @@ struct PrefillScoreMod {
     const float *slopes;           // [h_q]
     const int32_t *prefix_lens;    // [B] or null
     int window;                    // 0: no window
-    float cap_in, cap_out;         // as in ScoreModExt
+    float cap_in, cap_out;         // 2 scale log2(e) / cap and cap log2(e)
     float range;                   // |raw score| up to which the polynomial holds
     float c[3];                    // its coefficients, for raw scores and log2-domain logits
 

@@ -106,10 +106,15 @@ int split_launch_one(const SplitCall &c, const SplitParams &p, const typename Ex
     int rc = allow_smem(kernel, SC::smem_bytes(kSplitMaxSeqs), smem_set);
     if (rc != PA_OK) return rc;
     const int smem = SC::smem_bytes(c.num_seqs), sms = sm_count();
-    int per_sm = 0;
-    if (sms < 1 || cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, SC::THREADS, smem) != cudaSuccess ||
-        per_sm < 1)
-        return PA_ERR_CUDA;
+    static thread_local int known_smem = -1, known = 0;       // the last answer (the GPUs of a host are alike)
+    int per_sm = known;
+    if (sms < 1) return PA_ERR_CUDA;
+    if (known_smem != smem) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, SC::THREADS, smem) != cudaSuccess || per_sm < 1)
+            return PA_ERR_CUDA;
+        known_smem = smem;
+        known = per_sm;
+    }
     const int span = c.window > 0 ? std::min(c.window, c.max_context_len) : c.max_context_len;
     const int ctas = std::min(split_ctas_bound(c.num_seqs, c.h_kv, span), per_sm * sms);
     CUtensorMap mk, mv;

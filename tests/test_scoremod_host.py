@@ -58,7 +58,7 @@ def test_workspace_goes_by_the_window():
 @pytest.mark.parametrize("name,rng,terms,error", [("PA_TANH_C", "PA_TANH_RANGE", 3, 4e-7)])
 def test_polynomial_of_tanh(name, rng, terms, error):
     """tanh(y) = y q(y^2) on the range in which the kernel uses it."""
-    text = (Path(__file__).resolve().parents[1] / "paged_kv_cache_428_b200" / "csrc" / "scoremod.cuh").read_text()
+    text = (Path(__file__).resolve().parents[1] / "paged_kv_cache_428_b200" / "csrc" / "scoremod_prefill.cuh").read_text()
     get = lambda what: float(re.search(r"#define %s (-?[0-9.]+)f" % what, text).group(1))  # noqa: E731
     c, top = [get("%s%d" % (name, i)) for i in range(terms)], get(rng)
     worst = 0.0
