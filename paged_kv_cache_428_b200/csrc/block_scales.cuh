@@ -65,8 +65,7 @@ __device__ __forceinline__ uint32_t encode4(float x0, float x1, float x2, float 
 // one residual step (as in Markstein's division), q1 = q0 + (x - q0 s) r.  The residual is exact, so q1 is
 // within a step of the quotient, and is the quotient where that is an fp32 number.  Ties between two codes are
 // fp32 numbers, and every other quotient of 8-bit significands is further than that from a tie: the codes
-// are those of the division, at 3 instructions a value instead of about 12 (prompts of 37k tokens: 131 us with the
-// division, see the kernel below for what it takes now).  INT8: |q| <= 127 by the choice of the scale, and adding
+// are those of the division, at 3 instructions a value instead of about 12.  INT8: |q| <= 127 by the choice of the scale, and adding
 // 1.5 * 2^23 rounds it to nearest, ties to even, into the low byte.
 template <int QT>
 __device__ __forceinline__ uint32_t encode4_fast(float x0, float x1, float x2, float x3, float s, float r)
@@ -104,7 +103,7 @@ __device__ __forceinline__ uint32_t requantise4(uint32_t w, float was, float now
     return encode4<QT>(a.x * was, a.y * was, b.x * was, b.y * was, now);
 }
 
-constexpr int kScaleWriteWarps = 8;
+constexpr int kScaleWriteWarps = 4;
 constexpr int kScaleWriteMaxChunk = 64;
 
 __device__ __forceinline__ void team_sync(int team, int threads)
@@ -118,8 +117,11 @@ __device__ __forceinline__ void team_sync(int team, int threads)
 // K or V) at a time: the rows into registers, maximum over them, the scale, older rows requantised if it
 // grew, the rows' codes.  With TW = BS / (rows of 8 loads of a warp) a whole block is in the registers of its team
 // and its rows are read once; with TW = 1 (few tokens) a longer run's rows are read twice.
+//   37k tokens of 8 heads of 128 into INT8 blocks of 64, 229 MB: 131 us with a warp an item, rows read twice and IEEE
+// divisions; 77 us with teams and the residual step; 57 us with 8 CTAs of 4 warps an SM, one head each (66 at 4
+// CTAs of 8 warps and 4 heads), against 35 us for the bytes.  Issue slots and the latency of the lookups bound it.
 template <int D, int BS, int QT, int TW>
-__global__ void __launch_bounds__(kScaleWriteWarps * 32) write_block_scales_kernel(const BlockScaleWriteParams p)
+__global__ void __launch_bounds__(kScaleWriteWarps * 32, 8) write_block_scales_kernel(const BlockScaleWriteParams p)
 {
     constexpr unsigned FULL = 0xffffffffu;
     constexpr int LPR = D / 8, RPI = 32 / LPR;         // lanes per bf16 row, rows of one load
@@ -128,6 +130,7 @@ __global__ void __launch_bounds__(kScaleWriteWarps * 32) write_block_scales_kern
     constexpr int WORDS = (WINDOW + 31) / 32;
     __shared__ uint32_t border[WORDS + 1];             // bit i: token t0 + i does not continue the run of t0 + i - 1
     __shared__ int run_first[kScaleWriteMaxChunk], run_lo[kScaleWriteMaxChunk], run_hi[kScaleWriteMaxChunk];
+    __shared__ bool run_plain[kScaleWriteMaxChunk];    // row lo + i belongs to the run's token i
     __shared__ int num_runs;
     __shared__ int owner_of[kScaleWriteMaxChunk][BS];
     __shared__ uint32_t team_max[2][kScaleWriteWarps];
@@ -182,9 +185,13 @@ __global__ void __launch_bounds__(kScaleWriteWarps * 32) write_block_scales_kern
         }
         lo = __reduce_min_sync(FULL, lo);
         hi = __reduce_max_sync(FULL, hi);
+        bool plain = end - first == hi - lo + 1;
+        for (int i = first + lane; i < end && plain; i += 32) plain = (int)(p.slot_mapping[t0 + i] - blk * BS) - lo == i - first;
+        plain = __all_sync(FULL, plain);
         if (lane == 0) {
             run_lo[run] = lo;
             run_hi[run] = hi;
+            run_plain[run] = plain;
         }
     }
     __syncthreads();
@@ -207,11 +214,21 @@ __global__ void __launch_bounds__(kScaleWriteWarps * 32) write_block_scales_kern
         const float was = lo > 0 ? *scale : 0.f;       // a block written from its first row on has no older rows
         uint4 v[KEEP];
         auto row_of = [&](int base, int k) { return base + (member * KEEP + k) * RPI + sub; };
+        const bool plain = run_plain[run];
+        const uint4 *at = reinterpret_cast<const uint4 *>(rows + (t0 + run_first[run]) * stride) + col;
+        const int64_t step = stride / 8;               // of `at`, a row
         auto load = [&](int base) {
+            if (plain) {
+                const uint4 *from = at + (row_of(base, 0) - lo) * step;
 #pragma unroll
-            for (int k = 0; k < KEEP; ++k) {
-                const int row = row_of(base, k), t = row <= hi ? owner[row] : -1;
-                v[k] = t >= 0 ? __ldg(reinterpret_cast<const uint4 *>(rows + t * stride) + col) : make_uint4(0, 0, 0, 0);
+                for (int k = 0; k < KEEP; ++k, from += RPI * step)
+                    v[k] = row_of(base, k) <= hi ? __ldg(from) : make_uint4(0, 0, 0, 0);
+            } else {
+#pragma unroll
+                for (int k = 0; k < KEEP; ++k) {
+                    const int row = row_of(base, k), t = row <= hi ? owner[row] : -1;
+                    v[k] = t >= 0 ? __ldg(reinterpret_cast<const uint4 *>(rows + t * stride) + col) : make_uint4(0, 0, 0, 0);
+                }
             }
         };
         // maximum of |x|: the bits of finite bf16 magnitudes order like integers, two at a time
@@ -270,22 +287,23 @@ __global__ void __launch_bounds__(kScaleWriteWarps * 32) write_block_scales_kern
         const bool fast = finite && now >= 0x1p-100f && now <= 0x1p100f;
         const float r = __frcp_rn(now);
         const bool kept = hi - lo < ROWS;              // the rows are still in registers
-        for (int base = lo; base <= hi; base += ROWS) {
-            if (!kept) load(base);
+        auto store = [&](int base, auto encode) {
+            uint8_t *to = tile + (size_t)row_of(base, 0) * D + 8 * col;
 #pragma unroll
             for (int k = 0; k < KEEP; ++k) {
                 const int row = row_of(base, k);
-                if (row <= hi && owner[row] >= 0) {
+                if (row <= hi && (plain || owner[row] >= 0)) {
                     const float2 a = bf16x2_to_float2(v[k].x), b = bf16x2_to_float2(v[k].y);
                     const float2 c = bf16x2_to_float2(v[k].z), d = bf16x2_to_float2(v[k].w);
-                    uint2 code;
-                    if (fast)
-                        code = make_uint2(encode4_fast<QT>(a.x, a.y, b.x, b.y, now, r), encode4_fast<QT>(c.x, c.y, d.x, d.y, now, r));
-                    else
-                        code = make_uint2(encode4<QT>(a.x, a.y, b.x, b.y, now), encode4<QT>(c.x, c.y, d.x, d.y, now));
-                    reinterpret_cast<uint2 *>(tile + (size_t)row * D)[col] = code;
+                    *reinterpret_cast<uint2 *>(to + k * RPI * D) =
+                        make_uint2(encode(a.x, a.y, b.x, b.y), encode(c.x, c.y, d.x, d.y));
                 }
             }
+        };
+        for (int base = lo; base <= hi; base += ROWS) {
+            if (!kept) load(base);
+            if (fast) store(base, [&](float x, float y, float z, float w) { return encode4_fast<QT>(x, y, z, w, now, r); });
+            else store(base, [&](float x, float y, float z, float w) { return encode4<QT>(x, y, z, w, now); });
         }
     }
 }

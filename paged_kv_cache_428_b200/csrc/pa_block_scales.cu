@@ -65,9 +65,9 @@ int pa_reshape_and_cache_block_scales(const void *key, const void *value, int64_
     p.h_kv = h_kv;
     p.num_slots = (long long)num_blocks * block_size;
     // few tokens: as many CTAs as there is work for, each with about one (run, K or V) for a warp; many: whole
-    // runs for all warps, so that looking for the runs costs little beside the rows
+    // runs for teams of warps
     p.chunk = num_tokens <= 512 ? 4 : kScaleWriteMaxChunk;
-    p.heads = num_tokens <= 512 ? 1 : std::min(h_kv, 4);
+    p.heads = 1;
     const dim3 grid((num_tokens + p.chunk - 1) / p.chunk, (h_kv + p.heads - 1) / p.heads);
     if (grid.y > 65535) return PA_ERR_UNSUPPORTED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
