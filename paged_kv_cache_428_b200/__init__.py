@@ -543,15 +543,25 @@ def _split_workspace(workspace, size: int, device) -> torch.Tensor:
 
 def _need_decode(out, q, k_cache, v_cache, block_tables, context_lens, dtypes) -> tuple:
     """Checks of the split decodes; (num_seqs, h_q, head_dim, num_blocks, h_kv, block_size)."""
-    _need(out, "out", (torch.bfloat16,), 3)
-    _need(q, "q", (torch.bfloat16,), 3)
-    _need(k_cache, "k_cache", dtypes, 4)
-    _need(v_cache, "v_cache", (k_cache.dtype,), 4)
-    _need(block_tables, "block_tables", (torch.int32,), 2)
-    _need(context_lens, "context_lens", (torch.int32,), 1)
-    size, pool = q.shape, k_cache.shape
-    if out.shape != size or pool[3] != size[2] or v_cache.shape != pool or block_tables.shape[0] != size[0] \
-            or context_lens.shape[0] != size[0]:
+    bf16, i32 = torch.bfloat16, torch.int32
+    try:                                       # everything at once; what is wrong is found out below
+        size, pool = q.shape, k_cache.shape
+        fine = (q.dtype is bf16 and out.dtype is bf16 and k_cache.dtype in dtypes and v_cache.dtype is k_cache.dtype
+                and block_tables.dtype is i32 and context_lens.dtype is i32 and len(size) == 3 and len(pool) == 4
+                and block_tables.dim() == 2 and context_lens.dim() == 1 and q.is_cuda and q.is_contiguous()
+                and out.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+                and block_tables.is_contiguous() and context_lens.is_contiguous())
+    except AttributeError:
+        fine = False
+    if not fine:
+        _need(out, "out", (bf16,), 3)
+        _need(q, "q", (bf16,), 3)
+        _need(k_cache, "k_cache", dtypes, 4)
+        _need(v_cache, "v_cache", (k_cache.dtype,), 4)
+        _need(block_tables, "block_tables", (i32,), 2)
+        _need(context_lens, "context_lens", (i32,), 1)
+    if out.shape != size or pool[3] != size[2] or v_cache.shape != pool or len(block_tables) != size[0] \
+            or len(context_lens) != size[0]:
         raise ValueError("shape mismatch between out, q, caches, block_tables and context_lens")
     return *size, *pool[:3]
 

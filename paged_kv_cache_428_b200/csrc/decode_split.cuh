@@ -11,8 +11,10 @@
 // whatever the lengths are.  u is at least kSplitMinTokens tokens (a shorter range costs more in merging
 // than it saves) and at least 1/62 of the longest sequence, so that at most kSplitMaxPieces CTAs share one
 // (sequence, KV head) group.  Where the CTAs suffice for it, no range crosses the border of a group: each
-// group is cut into ceil(blocks / u) even pieces, short sequences need no merge, and no CTA ends two groups.  The
-// lengths are read on the device; the host's bound on them only sizes the grid.
+// group is cut into ceil(blocks / u) even pieces, and no CTA ends two groups; with no sequence longer than
+// kSplitWholeTokens each group is one piece, as its merge would take longer than its blocks (16 heads over 300
+// tokens: 7.2 us whole, 9.7 in pieces of 128; 32 heads over 1001 tokens: 14.6 and 10.6).  The lengths are read on
+// the device; the host's bound on them only sizes the grid.
 //   A producer warp streams the blocks' K and V tiles by 2-D TMA through an mbarrier ring, without a
 // pause between groups: lane j looks up triple j of the next 32 (and its scales) while the present 32
 // are issued.  Consumer warps take blocks in turn (mma.sync m16n8k16, tokens or head dims on
@@ -35,6 +37,7 @@ constexpr int kSplitMaxSeqs = 4096;       // sequences of one launch (block pref
 constexpr int kSplitMaxCtas = 1024;       // partial slots in the workspace: two for each of this many CTAs
 constexpr int kSplitMaxPieces = 64;       // CTAs that share one group
 constexpr int kSplitMinTokens = 128;      // tokens of the shortest range of one CTA
+constexpr int kSplitWholeTokens = 512;    // sequences up to this stay whole where there are CTAs enough
 constexpr int kSplitMaxGroups = 65536;    // (sequence, KV head) groups of one call: counters at the workspace's front
 
 struct SplitParams {
@@ -334,11 +337,11 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, SplitConfi
             *longest = most;
         }
         __syncwarp();
-        // cuts[s] = pieces of one KV head of the sequences before s, at the smallest u
-        const int u_min = max(kSplitMinTokens / BS, ceil_div(most, kSplitMaxPieces - 2));
+        // cuts[s] = pieces of one KV head of the sequences before s
+        const int u_cut = most * BS <= kSplitWholeTokens ? max(most, 1) : max(kSplitMinTokens / BS, ceil_div(most, kSplitMaxPieces - 2));
         carry = 0;
         for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
-            const int s = s0 + lane, n = s < p.num_seqs ? ceil_div(prefix[s + 1] - prefix[s], u_min) : 0;
+            const int s = s0 + lane, n = s < p.num_seqs ? ceil_div(prefix[s + 1] - prefix[s], u_cut) : 0;
             int sum = n;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -359,7 +362,7 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, SplitConfi
 
     const long long total = (long long)prefix[p.num_seqs] * p.h_kv;
     const int u_min = max(kSplitMinTokens / BS, ceil_div(*longest, kSplitMaxPieces - 2));
-    // pieces of u_min blocks at most, whole groups: this CTA's sequence and piece, if there are CTAs enough
+    // pieces of whole groups: this CTA's group and piece, if there are CTAs enough
     const bool aligned = (long long)cuts[p.num_seqs] * p.h_kv <= gridDim.x;
     long long u = 0, x0 = 0, x1 = 0;
     int first_cta = 0, group_pieces = 0;                       // aligned: of this CTA's group

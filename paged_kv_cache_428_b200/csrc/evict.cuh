@@ -75,22 +75,13 @@ __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const AddWeigh
     const size_t row = (size_t)seq * p.h_kv + kvh;
     const int t0 = blockIdx.x * kAddThreads * kAddPer + threadIdx.x;
     if ((int)blockIdx.x * kAddThreads * kAddPer >= n) return;
-    float lse[G];
-    bool fine = true;
-#pragma unroll
-    for (int h = 0; h < G; ++h) {
-        lse[h] = __ldcg(p.lse + row * G + h);
-        fine = fine && fabsf(lse[h]) < INFINITY;
-    }
-    if (!fine) return;
     const float *x = p.logits + row * p.row_tokens * G;
     float *w = p.weights + row * p.stride;
-    float v[kAddPer][G], old[kAddPer];
+    float v[kAddPer][G], old[kAddPer], lse[G];                 // all loads at once
 #pragma unroll
     for (int i = 0; i < kAddPer; ++i) {
         const int t = t0 + i * kAddThreads;
         if (t < n) {
-            old[i] = w[t];
             if constexpr (G % 4 == 0) {
 #pragma unroll
                 for (int h = 0; h < G; h += 4) {
@@ -104,8 +95,16 @@ __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const AddWeigh
 #pragma unroll
                 for (int h = 0; h < G; ++h) v[i][h] = __ldcg(x + (size_t)t * G + h);
             }
+            old[i] = w[t];
         }
     }
+    bool fine = true;
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+        lse[h] = __ldcg(p.lse + row * G + h);
+        fine = fine && fabsf(lse[h]) < INFINITY;
+    }
+    if (!fine) return;
 #pragma unroll
     for (int i = 0; i < kAddPer; ++i) {
         const int t = t0 + i * kAddThreads;

@@ -66,7 +66,7 @@ int pa_reshape_and_cache_block_scales(const void *key, const void *value, int64_
     p.num_slots = (long long)num_blocks * block_size;
     // few tokens: as many CTAs as there is work for, each with about one (run, K or V) for a warp; many: whole
     // runs for teams of warps
-    p.chunk = num_tokens <= 512 ? 4 : kScaleWriteMaxChunk;
+    p.chunk = num_tokens <= 512 ? 2 : kScaleWriteMaxChunk;
     p.heads = 1;
     const dim3 grid((num_tokens + p.chunk - 1) / p.chunk, (h_kv + p.heads - 1) / p.heads);
     if (grid.y > 65535) return PA_ERR_UNSUPPORTED;
