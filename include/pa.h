@@ -339,7 +339,7 @@ int pa_validate_slots(const int64_t *slot_mapping, int num_tokens, int block_siz
  * scores before the softmax.  With p the position of the query row (context_lens[s] - 1 for a decode
  * step) and t that of the key, in this order:
  *   x = scale * q . k
- *   softcap > 0:    x = softcap * tanh(x / softcap)      (0 = no cap; negative or not finite:
+ *   softcap > 0:    x = softcap * tanh(x / softcap)      (0 = no cap; else at least 2^-64 and finite, or
  *                   PA_ERR_INVALID_ARG)
  *   alibi_slopes:   x = x - alibi_slopes[h] * |p - t|    (device fp32 [h_q], finite; NULL = no bias)
  *   window > 0:     only tokens t > p - window are seen, the query's own among them (0 = no window)
@@ -351,7 +351,7 @@ int pa_validate_slots(const int64_t *slot_mapping, int num_tokens, int block_siz
  * says.
  * Blocks that lie before the window of every row of the call are not read: their table entries need not be
  * valid, so that a serving program can give them away.  bf16 caches (others: PA_ERR_UNSUPPORTED).
- * Accuracy as pa_decode and pa_prefill; tanh to an absolute 2^-22 of the cap.
+ * Accuracy as pa_decode and pa_prefill; a capped score to 2^-19 of itself or 2^-22 of the cap.
  *
  * pa_decode_scoremod: arguments as pa_decode.  workspace as in pa_decode_block_scales, of
  * pa_decode_scoremod_workspace_size(...) bytes; the same limits. */
@@ -383,7 +383,7 @@ int pa_prefill_scoremod(void *out, const void *q, const void *k_cache, const voi
  * that gets rows, and each KV head, with QMAX = 448 (E4M3) or 127 (INT8) and `first` the lowest
  * offset in the block that this call writes:
  *   - s = the smallest bf16 number with QMAX * s >= max|x| over the block's new rows (infinities and
- *     NaN left out);
+ *     NaN left out), at least 2^-80 unless that maximum is 0;
  *   - first = 0: the block begins anew, scale = s;
  *   - first > 0: scale = max(old scale, s).  If it grew, the rows below `first` are requantised,
  *     code = rne(code * old scale / scale); rows above the new ones stay as they are.
@@ -414,7 +414,8 @@ int pa_validate_block_runs(const int64_t *slot_mapping, int num_tokens, int bloc
 
 /* pa_decode over such a cache.  Same result as pa_decode over the values code * scale: fp32 sums,
  * probabilities rounded to fp16 (2^-11) for the product with the codes, relative to the largest
- * probability * V scale, so that blocks with very different scales add up without loss.
+ * probability * V scale, so that blocks with very different scales add up without loss.  V scales are
+ * finite and at least 2^-80, or 0 (a block whose codes are all 0), as the write leaves them.
  *   max_context_len  host-known bound of context_lens; it only sizes the grid
  *   workspace      device, >= pa_decode_block_scales_workspace_size(...) bytes, 16-byte aligned, zero before
  *                  its first use; every call leaves it ready for the next one, of whatever sizes, here

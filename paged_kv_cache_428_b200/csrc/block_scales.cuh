@@ -2,7 +2,7 @@
 // the write that keeps the scales, and what the decode of decode_split.cuh needs to know.
 //
 // The scale of a block is the smallest bf16 number s with QMAX s >= max|x| over the block's rows (QMAX = 448
-// for E4M3, 127 for INT8), kept in fp32.  A code is x / s to nearest, ties to even.  With 8 significant
+// for E4M3, 127 for INT8), but at least 2^-80 unless all of them are 0, kept in fp32.  A code is x / s to nearest, ties to even.  With 8 significant
 // bits in x and in s, and at most 7 in a code, x / s and code * s_old / s_new round in fp32 exactly as in
 // any wider type (a quotient of such numbers that is not a tie is further from one than 2^-17 of it):
 // codes are what the definition says, bit for bit.  Against max|x| / QMAX itself the scale is at most 2^-7
@@ -35,11 +35,13 @@ struct BlockScaleWriteParams {
 template <int QT>
 __device__ __forceinline__ constexpr float code_max() { return QT == 1 ? 448.f : 127.f; }
 
-// The smallest bf16 value that is not below amax / QMAX (fp32 division: exact enough, see above).
+// The smallest bf16 value that is not below amax / QMAX (fp32 division: exact enough, see above).  Its floor keeps
+// what the decode adds up, 2^15 / scale for each token, inside fp32.
 template <int QT>
 __device__ __forceinline__ float block_scale_of(float amax)
 {
-    return __uint_as_float((__float_as_uint(__fdiv_rn(amax, code_max<QT>())) + 0xffffu) & 0xffff0000u);
+    const float s = __uint_as_float((__float_as_uint(__fdiv_rn(amax, code_max<QT>())) + 0xffffu) & 0xffff0000u);
+    return s > 0.f ? fmaxf(s, kMinBlockScale) : 0.f;
 }
 
 template <int QT>

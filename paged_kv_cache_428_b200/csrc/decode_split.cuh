@@ -38,6 +38,7 @@ constexpr int kSplitMaxCtas = 1024;       // partial slots in the workspace: two
 constexpr int kSplitMaxPieces = 64;       // CTAs that share one group
 constexpr int kSplitMinTokens = 128;      // tokens of the shortest range of one CTA
 constexpr int kSplitWholeTokens = 512;    // sequences up to this stay whole where there are CTAs enough
+constexpr float kMinBlockScale = 0x1p-80f;    // of a block of codes, unless it is 0
 constexpr int kSplitMaxGroups = 65536;    // (sequence, KV head) groups of one call: counters at the workspace's front
 
 struct SplitParams {
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, SplitConfi
             float v_log2 = 0.f, v_inv = 1.f;
             if constexpr (QT != 0) {
                 // a block whose V codes are all 0 has scale 0: any scale stands for it
-                const float v = vs > 0.f ? vs : 1.f;
+                const float v = vs > 0.f ? fmaxf(vs, kMinBlockScale) : 1.f;
                 v_log2 = log2f(v);
                 v_inv = 1.f / v;
             }

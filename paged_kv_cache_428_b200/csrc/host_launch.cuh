@@ -215,8 +215,8 @@ int collect_device_errors(unsigned int *flags, int clear)
     return PA_OK;
 }
 
-// tanh cap of the scores: 0 = none.
-bool valid_softcap(float cap) { return std::isfinite(cap) && cap >= 0.f; }
+// tanh cap of the scores: 0 = none (below 2^-64 its inverse times a score would leave fp32).
+bool valid_softcap(float cap) { return std::isfinite(cap) && (cap == 0.f || cap >= 0x1p-64f); }
 
 }  // namespace
 

@@ -88,7 +88,7 @@ int pa_decode_weights(void *out, float *weights, int64_t weights_stride, const v
     p.lse = reinterpret_cast<float *>(ws + lay.lse);
     const WeightsExt::Args args{reinterpret_cast<float *>(ws + lay.end), logit_tokens(max_context_len)};
     rc = split_launch<0, WeightsExt>(c, p, args);
-    if (rc != PA_OK || max_context_len == 0) return rc;
+    if (rc != PA_OK) return rc;
     AddWeightsParams a{};
     a.logits = args.logits;
     a.lse = p.lse;
@@ -98,7 +98,7 @@ int pa_decode_weights(void *out, float *weights, int64_t weights_stride, const v
     a.max_tokens = max_context_len;
     a.row_tokens = args.row_tokens;
     a.h_kv = h_kv;
-    const dim3 grid((max_context_len + kAddThreads * kAddPer - 1) / (kAddThreads * kAddPer), h_kv, num_seqs);
+    const dim3 grid(std::max(1, (max_context_len + kAddThreads * kAddPer - 1) / (kAddThreads * kAddPer)), h_kv, num_seqs);
     return switch_group(h_q / h_kv, [&](auto gc) {
         return launch_ex(add_weights_kernel<decltype(gc)::value>, grid, dim3(kAddThreads), 0,
                          static_cast<cudaStream_t>(stream), true, a);

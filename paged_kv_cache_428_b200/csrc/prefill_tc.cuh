@@ -520,6 +520,19 @@ __global__ void __launch_bounds__(PrefillTcConfig<D, BS, G, NQ_, KST_, VST_>::TH
                 const bool tail = is_v && ((tile + 1) * BN > ctx || head);
                 uint64_t *bar = tail ? v_tail : &full[st];
                 uint8_t *dst = smem + (is_v ? C::OFF_V : C::OFF_K) + st * C::KV_TILE;
+                if constexpr (Mod::kOn) {
+                    // K rows of blocks that are not copied: 0 and not what an earlier item left there, as all
+                    // scores of a tile have a say in how tanh is computed
+                    if (Mod::kCap && !is_v && (skip > 0 || nb < BPT)) {
+                        const int n8 = skip * BS * 8, m8 = (BN - nb * BS) * 8;
+                        for (int idx = lane; idx < C::HALVES * (n8 + m8); idx += 32) {
+                            const int h = idx / (n8 + m8), i = idx % (n8 + m8), i8 = i < n8 ? i : nb * BS * 8 + i - n8;
+                            *reinterpret_cast<uint4 *>(dst + h * C::KV_HALF + i8 * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                }
                 if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)((nb - skip) * C::HALVES * BS * 128));
                 __syncwarp();
                 if (mine)

@@ -11,6 +11,7 @@
 #pragma once
 
 #include "prefill_tc.cuh"
+#include "tanh_poly.cuh"
 
 namespace pa {
 
@@ -27,15 +28,9 @@ __device__ __forceinline__ float rcp_approx(float x)
 //   BIAS               one multiply-add to the raw score, slope / scale times the place in the tile; what the
 //                      whole tile has in common goes into the softmax's reference.  Only tiles with tokens on
 //                      both sides of a row need more.
-//   CAP                tanh(y) = y q(y^2) while a warp's tile has |x| <= 0.3 cap, q of degree 2 interpolating
-//                      tanh(y) / y at the Chebyshev nodes of [0, 0.09] in y^2 (absolute error below 4e-7), with
-//                      cap and scale inside the coefficients, on the FMA pipe; else the exact form, an
-//                      exponential and a reciprocal more for each score on the MUFU unit.
-#define PA_TANH_RANGE 0.3f
-#define PA_TANH_C0 0.99999883513f
-#define PA_TANH_C1 -0.33309988804f
-#define PA_TANH_C2 0.12633582392f
-
+//   CAP                tanh(y) = y q(y^2) while a warp's tile has |x| <= 0.3 cap (see tanh_poly.cuh), with cap and
+//                      scale inside the coefficients, on the FMA pipe; else the exact form, an exponential and
+//                      a reciprocal more for each score on the MUFU unit.
 // Places of a tile's tokens, two at a time (operands of one packed multiply-add each).
 __constant__ float2 kPlaces[32] = {
     {0.f, 1.f}, {2.f, 3.f}, {4.f, 5.f}, {6.f, 7.f}, {8.f, 9.f}, {10.f, 11.f}, {12.f, 13.f}, {14.f, 15.f},
@@ -45,7 +40,7 @@ __constant__ float2 kPlaces[32] = {
 
 template <bool CAP, bool BIAS>
 struct PrefillScoreMod {
-    static constexpr bool kOn = true;
+    static constexpr bool kOn = true, kCap = CAP;
     const float *slopes;           // [h_q]
     const int32_t *prefix_lens;    // [B] or null
     int window;                    // 0: no window

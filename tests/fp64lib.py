@@ -11,12 +11,12 @@ DTYPE = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8}
 
 
 def block_scale(amax: float, kind: str) -> float:
-    """The smallest bf16 number s with QMAX s >= amax."""
+    """The smallest bf16 number s with QMAX s >= amax, at least 2^-80 unless amax is 0."""
     if amax == 0:
         return 0.0
     want = amax / QMAX[kind]
     unit = 2.0 ** (max(math.floor(math.log2(want)), -126) - 7)
-    return math.ceil(want / unit) * unit
+    return max(math.ceil(want / unit) * unit, 2.0 ** -80)
 
 
 def encode(x: torch.Tensor, s: float, kind: str) -> torch.Tensor:

@@ -115,6 +115,28 @@ def test_write_values_where_it_can_go_wrong(kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+def test_tiny_values_beside_ordinary_ones(kind):
+    """Blocks of values near and below the floor of the scales, alone and beside blocks of ordinary ones: written as
+    defined, and the attention over both is that over code * scale."""
+    g, h, d, bs = _gen(13), 2, 64, 16
+    c = Cache(12, h, bs, d, kind)
+    order = [3, 7, 1, 9, 0, 5]
+    k, v = _rows(96, h, d, g), _rows(96, h, d, g)
+    for b, f in ((1, 2.0 ** -90), (3, 2.0 ** -120), (4, 2.0 ** -70)):
+        v[16 * b:16 * b + 16] *= f
+    k[32:48] *= 2.0 ** -100
+    c.write(k, v, _slots(order, 0, 96, bs))
+    c.check()
+    q = (torch.randn((3, 4 * h, d), generator=g) * 0.5).to(torch.bfloat16)
+    tab = torch.full((3, 6), -1, dtype=torch.int32)
+    tab[0] = torch.tensor(order, dtype=torch.int32)
+    tab[1, :2] = torch.tensor([order[1], order[3]], dtype=torch.int32)       # tiny ones only
+    tab[2, :1] = order[4]
+    case = (q, (c.k.cpu(), c.v.cpu()), (c.ks.cpu(), c.vs.cpu()), tab, torch.tensor([96, 32, 10], dtype=torch.int32))
+    _check(case, _run(case))
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_write_ratios_that_are_ties(kind):
     """Scales that grow by simple ratios: requantised codes fall on ties of the rounding."""
     h, d, bs = 1, 128, 16

@@ -122,6 +122,10 @@ def test_decode_weights_add_up_and_bounds():
     out = _decode(q, k, v, tab, ctx, w, max_len=50)
     assert pa.pa_device_errors() == pa.PA_DEVERR_BAD_LENGTH
     _check_decode(q, k, v, tab, lens, out, w, before, counted=50)
+    # no tokens counted at all
+    w = torch.ones((2, 2, 3), device=DEV)
+    out = _decode(q, k, v, tab, ctx, w, max_len=0)
+    assert pa.pa_device_errors() == pa.PA_DEVERR_BAD_LENGTH and bool((w == 1).all()) and torch.isfinite(out).all()
     # a block outside the pool: the row is NaN and its weights stay
     bad = tab.clone()
     bad[0, 2] = -1
@@ -255,6 +259,40 @@ def test_evict_weights_that_are_alike(what, n):
     elif what == "two":
         w = torch.where(torch.rand(w.shape, generator=g) < 0.5, 1.0, 1.0 + 2.0 ** -23)
     _evict_case([n], 2, 16, 64, 250, 20, 3, weights=w, stride=n)
+
+
+def test_evict_captured_and_on_another_stream():
+    g = _gen(9)
+    lens = [700, 90, 3]
+    k, v, tab, free = _pool(lens, 20, 2, 16, 64, g)
+    new_tab = torch.tensor(free[:15], dtype=torch.int32, device=DEV).view(3, 5)
+    w = torch.rand((3, 2, 700), generator=g).to(DEV)
+    tab, ctx = tab.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV)
+
+    def buffers():
+        return (k.to(DEV), v.to(DEV), torch.zeros((3, 2, 70), dtype=torch.int32, device=DEV),
+                torch.zeros((3, 2, 80), device=DEV), torch.zeros(3, dtype=torch.int32, device=DEV))
+
+    def call(b, **kw):
+        pa.pa_evict(b[0], b[1], w, tab, ctx, new_tab, 700, 70, 9, b[2], b[3], b[4], **kw)
+
+    first, second, third = buffers(), buffers(), buffers()
+    call(first)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    call(second, stream=side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(third)
+    for _ in range(2):
+        for t in third[2:]:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+    for other in (second, third):
+        for a, b in zip(first, other):
+            assert torch.equal(a.nan_to_num(nan=5.0), b.nan_to_num(nan=5.0))
 
 
 def test_evict_bad_blocks_and_lengths():

@@ -110,6 +110,13 @@ def test_decode_large_scores():
     _decode([200, 33], 2, 4, 16, 128, 4, softcap=3.0, q_factor=300.0)
 
 
+@pytest.mark.parametrize("softcap", [2.0 ** -64, 1e3, 1e6, 1e20])
+def test_caps_far_from_the_scores(softcap):
+    """A cap far above the scores leaves them as they are; one far below leaves their signs."""
+    _decode([200, 33], 2, 4, 16, 64, 14, softcap=softcap)
+    _prefill([60, 0], [80, 30], 2, 4, 16, 64, 14, softcap=softcap)
+
+
 def test_decode_without_any_is_decode():
     gen = _gen(5)
     k, v, tab, _ = _pool([400, 77], 2, 16, 128, gen)
@@ -198,6 +205,23 @@ def test_prefill_cap_of_any_size(softcap, q_factor):
 @pytest.mark.parametrize("kw", [dict(softcap=50.0, window=1024), dict(alibi=True, prefix=[200, 900]), dict(window=300, alibi=True)])
 def test_prefill_large(kw):
     _prefill([3584, 700], [512, 2048], 2, 4, 16, 128, 9, rows=12, **kw)
+
+
+def test_prefill_does_not_depend_on_what_lies_in_masked_places():
+    """The same call before and after calls that leave very large K and V in shared memory, and with other
+    garbage in the slots that hold no token: the same bits, whichever way tanh is computed."""
+    kw = dict(softcap=8.0, window=50, q_factor=0.7, rows=4)
+    lens = ([130, 77, 300], [70, 130, 20])
+    first = _prefill(*lens, 2, 4, 16, 128, 15, **kw)
+    gen = _gen(16)
+    big = (torch.randn((64, 2, 16, 128), generator=gen) * 1e4).to(torch.bfloat16).to(DEV)
+    q = (torch.randn((2000, 8, 128), generator=gen) * 1e4).to(torch.bfloat16).to(DEV)
+    tab = torch.arange(64, dtype=torch.int32, device=DEV).view(1, 64).repeat(16, 1)
+    start = torch.arange(0, 2001, 125, dtype=torch.int32, device=DEV)
+    for _ in range(3):
+        pa.pa_prefill_scoremod(torch.empty_like(q), q, big, big, tab, start, torch.full((16,), 1000, dtype=torch.int32, device=DEV),
+                               125, pa.make_prefill_workspace(), softcap=8.0)
+        assert torch.equal(first, _prefill(*lens, 2, 4, 16, 128, 15, **kw))
 
 
 def test_prefill_more_sequences_than_the_claim_order_keeps():

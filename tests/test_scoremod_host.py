@@ -24,7 +24,7 @@ def _decode(**kw):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(cap=-1.0), -1), (dict(cap=NAN), -1), (dict(cap=INF), -1), (dict(win=-1), -1), (dict(dt=1), -2), (dict(dt=9), -1),
+    (dict(cap=-1.0), -1), (dict(cap=NAN), -1), (dict(cap=INF), -1), (dict(cap=2.0 ** -65), -1), (dict(win=-1), -1), (dict(dt=1), -2), (dict(dt=9), -1),
     (dict(scale=NAN), -1), (dict(hq=5), -1), (dict(hq=32), -2), (dict(d=256), -2), (dict(bs=1), -2), (dict(B=5000), -2),
     (dict(out=0), -1), (dict(ctx=0), -1), (dict(ws=0), -3), (dict(wsb=100), -3), (dict(B=0), 0), (dict(B=0, cap=-1.0), -1)])
 def test_decode_refusals(kw, status):
@@ -58,17 +58,19 @@ def test_workspace_goes_by_the_window():
 @pytest.mark.parametrize("name,rng,terms,error", [("PA_TANH_C", "PA_TANH_RANGE", 3, 4e-7)])
 def test_polynomial_of_tanh(name, rng, terms, error):
     """tanh(y) = y q(y^2) on the range in which the kernel uses it."""
-    text = (Path(__file__).resolve().parents[1] / "paged_kv_cache_428_b200" / "csrc" / "scoremod_prefill.cuh").read_text()
+    text = (Path(__file__).resolve().parents[1] / "paged_kv_cache_428_b200" / "csrc" / "tanh_poly.cuh").read_text()
     get = lambda what: float(re.search(r"#define %s (-?[0-9.]+)f" % what, text).group(1))  # noqa: E731
     c, top = [get("%s%d" % (name, i)) for i in range(terms)], get(rng)
-    worst = 0.0
+    worst = relative = 0.0
     for i in range(20001):
         y = top * i / 20000
         q = 0.0
         for a in reversed(c):
             q = q * y * y + a
         worst = max(worst, abs(y * q - math.tanh(y)))
-    assert worst < error
+        if y:
+            relative = max(relative, abs(y * q / math.tanh(y) - 1))
+    assert worst < error and relative < 1.2e-6
 
 
 def test_binding_refuses():
