@@ -13,6 +13,11 @@ Functions keep the C names:
 * :func:`pa_decode` -- split-context decode attention through the block table
   (= :func:`pa_decode_partitions` + :func:`pa_decode_merge`)
 * :func:`pa_copy_blocks` -- copy-on-write block copy over all layers
+* :func:`pa_decode_scoremod`, :func:`pa_prefill_scoremod` -- attention with capped, biased, windowed scores
+* :func:`pa_reshape_and_cache_block_scales`, :func:`pa_decode_block_scales` -- 8-bit cache, a scale per
+  (block, KV head)
+* :func:`pa_decode_weights`, :func:`pa_evict` -- decode that counts what cached tokens are worth, and
+  eviction by it
 * :class:`BlockAllocator` -- the host block allocator (free pool, refcounts,
   fork, copy-on-write decisions) that builds block tables and slot ids
 """

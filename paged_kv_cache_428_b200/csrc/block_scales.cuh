@@ -67,26 +67,25 @@ __device__ __forceinline__ uint32_t encode4(float x0, float x1, float x2, float 
 // one residual step (as in Markstein's division), q1 = q0 + (x - q0 s) r.  The residual is exact, so q1 is
 // within a step of the quotient, and is the quotient where that is an fp32 number.  Ties between two codes are
 // fp32 numbers, and every other quotient of 8-bit significands is further than that from a tie: the codes
-// are those of the division, at 3 instructions a value instead of about 12.  INT8: |q| <= 127 by the choice of the scale, and adding
+// are those of the division, at 3 packed instructions for two values instead of about 24.  INT8: |q| <= 127 by the choice of the scale, and adding
 // 1.5 * 2^23 rounds it to nearest, ties to even, into the low byte.
 template <int QT>
 __device__ __forceinline__ uint32_t encode4_fast(float x0, float x1, float x2, float x3, float s, float r)
 {
-    auto divide = [&](float x) {
-        const float q = x * r;
-        return fmaf(fmaf(-q, s, x), r, q);
+    const float2 r2 = make_float2(r, r), s2 = make_float2(-s, -s);
+    auto divide = [&](float2 x) {
+        const float2 q = __fmul2_rn(x, r2);
+        return __ffma2_rn(__ffma2_rn(q, s2, x), r2, q);
     };
-    x0 = divide(x0);
-    x1 = divide(x1);
-    x2 = divide(x2);
-    x3 = divide(x3);
+    float2 a = divide(make_float2(x0, x1)), b = divide(make_float2(x2, x3));
     if constexpr (QT == 1) {
-        return pack_codes<1>(x0, x1, x2, x3);
+        return pack_codes<1>(a.x, a.y, b.x, b.y);
     } else {
-        constexpr float R = 12582912.f;                // 1.5 * 2^23
-        const uint32_t a = __byte_perm(__float_as_uint(x0 + R), __float_as_uint(x1 + R), 0x0040);
-        const uint32_t b = __byte_perm(__float_as_uint(x2 + R), __float_as_uint(x3 + R), 0x0040);
-        return __byte_perm(a, b, 0x5410);
+        const float2 R = make_float2(12582912.f, 12582912.f);      // 1.5 * 2^23
+        a = __fadd2_rn(a, R);
+        b = __fadd2_rn(b, R);
+        return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                           __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
     }
 }
 
@@ -233,14 +232,18 @@ __global__ void __launch_bounds__(kScaleWriteWarps * 32, 8) write_block_scales_k
                 }
             }
         };
-        // maximum of |x|: the bits of finite bf16 magnitudes order like integers, two at a time
+        // maximum of |x|, two at a time; NaN stays in it
+        auto max2 = [](uint32_t a, uint32_t b) {
+            const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
+            return *reinterpret_cast<const uint32_t *>(&m);
+        };
         uint32_t top = 0;
         for (int base = lo; base <= hi; base += ROWS) {
             load(base);
 #pragma unroll
             for (int k = 0; k < KEEP; ++k) {
-                top = __vmaxu2(top, __vmaxu2(v[k].x & 0x7fff7fffu, v[k].y & 0x7fff7fffu));
-                top = __vmaxu2(top, __vmaxu2(v[k].z & 0x7fff7fffu, v[k].w & 0x7fff7fffu));
+                top = max2(top, max2(v[k].x & 0x7fff7fffu, v[k].y & 0x7fff7fffu));
+                top = max2(top, max2(v[k].z & 0x7fff7fffu, v[k].w & 0x7fff7fffu));
             }
         }
         auto over_team = [&](uint32_t m, int slot) {   // the maximum over the team's threads
