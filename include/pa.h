@@ -351,7 +351,7 @@ int pa_validate_slots(const int64_t *slot_mapping, int num_tokens, int block_siz
  * says.
  * Blocks that lie before the window of every row of the call are not read: their table entries need not be
  * valid, so that a serving program can give them away.  bf16 caches (others: PA_ERR_UNSUPPORTED).
- * Accuracy as pa_decode and pa_prefill; a capped score to 2^-19 of itself or 2^-22 of the cap.
+ * Accuracy as pa_decode and pa_prefill; a capped score to 2^-19 of itself or 2^-20 of the cap.
  *
  * pa_decode_scoremod: arguments as pa_decode.  workspace as in pa_decode_block_scales, of
  * pa_decode_scoremod_workspace_size(...) bytes; the same limits. */

@@ -594,6 +594,14 @@ def pa_decode_scoremod_workspace_size(num_seqs: int, h_q: int, h_kv: int, head_d
     return int(_lib.pa_decode_scoremod_workspace_size(num_seqs, h_q, h_kv, head_dim, max_context_len, window))
 
 
+def _window(window) -> int:
+    """A window in tokens that fits the call's 32 bits."""
+    w = int(window)
+    if w < 0:
+        raise ValueError("window must be 0 (none) or a number of tokens, got %d" % w)
+    return min(w, 2 ** 31 - 1)
+
+
 def _slopes_ptr(alibi_slopes, h_q: int) -> Optional[int]:
     if alibi_slopes is None:
         return None
@@ -609,12 +617,13 @@ def pa_decode_scoremod(out, q, k_cache, v_cache, block_tables, context_lens, max
     """pa_decode with scores capped by softcap * tanh(x / softcap), less alibi_slopes[h] times the distance, over
     the last `window` tokens; each is off by default.  Returns out."""
     B, h_q, d, NB, h_kv, bs = _need_decode(out, q, k_cache, v_cache, block_tables, context_lens, CACHE_DTYPES)
+    window = _window(window)
     ws = _split_workspace(workspace, 0 if workspace is not None else pa_decode_scoremod_workspace_size(
         B, h_q, h_kv, d, max_context_len, window), q.device)
     _check(_lib.pa_decode_scoremod(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         block_tables.shape[1], context_lens.data_ptr(), B, int(max_context_len), h_q, h_kv, d, bs, NB,
-        1.0 / math.sqrt(d) if scale is None else float(scale), float(softcap), _slopes_ptr(alibi_slopes, h_q), int(window),
+        1.0 / math.sqrt(d) if scale is None else float(scale), float(softcap), _slopes_ptr(alibi_slopes, h_q), window,
         cache_dtype_code(k_cache), ws.data_ptr(), ws.numel(),
         _on_current_device(stream, out, q, k_cache, v_cache, block_tables, context_lens, alibi_slopes, ws)),
         "pa_decode_scoremod")
@@ -634,7 +643,7 @@ def pa_prefill_scoremod(out, q, k_cache, v_cache, block_tables, query_start, con
         if prefix_lens.shape[0] != context_lens.shape[0]:
             raise ValueError("prefix_lens: expected %d, got %d" % (context_lens.shape[0], prefix_lens.shape[0]))
     _check(_lib.pa_prefill_scoremod(
-        *a[:16], float(softcap), _slopes_ptr(alibi_slopes, q.shape[1]), int(window),
+        *a[:16], float(softcap), _slopes_ptr(alibi_slopes, q.shape[1]), _window(window),
         None if prefix_lens is None else prefix_lens.data_ptr(), a[16], workspace.data_ptr(), workspace.numel(),
         _on_current_device(stream, out, q, k_cache, v_cache, block_tables, query_start, context_lens, alibi_slopes,
                            prefix_lens, workspace)), "pa_prefill_scoremod")

@@ -110,6 +110,50 @@ def test_decode_large_scores():
     _decode([200, 33], 2, 4, 16, 128, 4, softcap=3.0, q_factor=300.0)
 
 
+def test_a_cache_past_32_bits():
+    """Blocks whose elements lie past 2^32 bytes and 2^31 elements, in a pool that is mostly untouched memory."""
+    nb, h, bs, d, n = 1 << 19, 4, 16, 128, 150
+    assert nb * h * bs * d > 2 ** 31
+    gen = _gen(17)
+    kc, vc = (torch.empty((nb, h, bs, d), dtype=torch.bfloat16, device=DEV) for _ in "kv")
+    k, v = (torch.randn((n, h, d), generator=gen).to(torch.bfloat16) for _ in "kv")
+    blocks = torch.tensor([nb - 1 - 3 * i for i in range(10)])
+    t = torch.arange(n)
+    pa.pa_reshape_and_cache(k.to(DEV), v.to(DEV), kc, vc, (blocks[t // bs] * bs + t % bs).to(DEV))
+    tab = blocks.int().view(1, 10).to(DEV)
+    ctx = torch.tensor([n], dtype=torch.int32, device=DEV)
+    q = torch.randn((n, h * 2, d), generator=gen).to(torch.bfloat16)
+    rk, rv = k.double().transpose(0, 1), v.double().transpose(0, 1)
+    o, mag, _ = ref.attend(q, rk, rv, t, 1 / math.sqrt(d), 10.0, None, 60)
+    err = _logit_error(q, rk, 1 / math.sqrt(d), 10.0, None, d)
+    out, one = torch.empty_like(q, device=DEV), torch.empty_like(q[:1], device=DEV)
+    pa.pa_prefill_scoremod(out, q.to(DEV), kc, vc, tab, torch.tensor([0, n], dtype=torch.int32, device=DEV), ctx, n,
+                           pa.make_prefill_workspace(), softcap=10.0, window=60)
+    pa.pa_decode_scoremod(one, q[-1:].to(DEV), kc, vc, tab, ctx, n, softcap=10.0, window=60)
+    ref.check_rows(out, o, mag, 8, "prefill", err)
+    ref.check_rows(one, o[-1:], mag[-1:], 8, "decode", err)
+    # eviction from there to there
+    w = torch.rand((1, h, n), generator=gen).to(DEV)
+    fresh = torch.tensor([[nb - 2, nb - 50]], dtype=torch.int32, device=DEV)
+    kept, nw = torch.empty((1, h, 30), dtype=torch.int32, device=DEV), torch.empty((1, h, 30), device=DEV)
+    pa.pa_evict(kc, vc, w, tab, ctx, fresh, n, 30, 4, kept, nw, ctx.clone())
+    for i in range(h):
+        rows = k[kept[0, i].cpu().long(), i]
+        assert torch.equal(torch.cat([kc[nb - 2, i], kc[nb - 50, i, :14]]).cpu(), rows)
+    # and a block-scaled write and decode past 2^31 bytes of codes
+    del kc, vc
+    kq, vq = (torch.empty((nb, h, bs, d), dtype=torch.int8, device=DEV) for _ in "kv")
+    ks, vs = pa.make_block_scales(nb, h)
+    pa.pa_reshape_and_cache_block_scales(k.to(DEV), v.to(DEV), kq, vq, ks, vs, (blocks[t // bs] * bs + t % bs).to(DEV))
+    pa.pa_decode_block_scales(one, q[-1:].to(DEV), kq, vq, ks, vs, tab, ctx, n)
+    b = blocks.to(DEV)
+    rk, rv = ((c[b].double() * s[b].double()[:, :, None, None]).permute(1, 0, 2, 3).reshape(h, -1, d)[:, :n].cpu()
+              for c, s in ((kq, ks), (vq, vs)))
+    o, mag, _ = ref.attend(q[-1:], rk, rv, t[-1:], 1 / math.sqrt(d))
+    ref.check_rows(one, o, mag, 11, "codes", extra=2.0 ** -40 * 127 * float(vs.max()) * n)
+    assert pa.pa_device_errors() == 0
+
+
 @pytest.mark.parametrize("softcap", [2.0 ** -64, 1e3, 1e6, 1e20])
 def test_caps_far_from_the_scores(softcap):
     """A cap far above the scores leaves them as they are; one far below leaves their signs."""

@@ -79,5 +79,8 @@ def test_binding_refuses():
     i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
     with pytest.raises(ValueError):                                   # CPU tensors
         pa.pa_decode_scoremod(q, q, c, c, i32(1, 2), i32(1), 32)
+    assert pa._window(2 ** 40) == 2 ** 31 - 1 and pa._window(0) == 0
+    with pytest.raises(ValueError):
+        pa._window(-1)
     with pytest.raises(TypeError):
         pa.pa_decode_scoremod(q.float(), q, c, c, i32(1, 2), i32(1), 32)
