@@ -255,15 +255,17 @@ struct SplitPlace {
     int seq, kvh, block, nb;       // block: within the group's nb blocks
 };
 
-// The blocks of sequence s that its window leaves: the first one, and how many.  A context longer than
+// The blocks of a sequence that its window leaves: the first one, and how many.  A context longer than
 // the table row counts one block past the row, which is then reported as bad.
-__device__ __forceinline__ void split_blocks(int ctx, int window, int bs, int max_blocks, int &first, int &count)
+__host__ __device__ __forceinline__ void split_blocks(int ctx, int window, int bs, int max_blocks, int &first, int &count)
 {
     first = window > 0 && ctx > window ? (ctx - window) / bs : 0;
-    count = ctx > 0 ? min((ctx - 1) / bs + 1, max(max_blocks, first) + 1) - first : 0;
+    count = ctx > 0 ? cmin((ctx - 1) / bs + 1, cmax(max_blocks, first) + 1) - first : 0;
 }
 
-__device__ __forceinline__ SplitPlace split_locate(const int *prefix, int num_seqs, int h_kv, long long x)
+// prefix[s]: blocks (or pieces) of one KV head of the sequences before s, num_seqs + 1 entries.  x: below
+// prefix[num_seqs] * h_kv.
+__host__ __device__ __forceinline__ SplitPlace split_locate(const int *prefix, int num_seqs, int h_kv, long long x)
 {
     int lo = 0, hi = num_seqs - 1;                     // the last sequence whose triples start at or before x
     while (lo < hi) {
@@ -278,6 +280,61 @@ __device__ __forceinline__ SplitPlace split_locate(const int *prefix, int num_se
     at.kvh = (int)(rem / at.nb);
     at.block = (int)(rem - (long long)at.kvh * at.nb);
     return at;
+}
+
+// Blocks of the shortest range, and of the largest piece of a whole group, when the longest sequence has
+// `longest` of them.
+__host__ __device__ __forceinline__ int split_shortest(int longest, int bs)
+{
+    return cmax(kSplitMinTokens / bs, ceil_div(longest, kSplitMaxPieces - 2));
+}
+__host__ __device__ __forceinline__ int split_piece(int longest, int bs)
+{
+    return (long long)longest * bs <= kSplitWholeTokens ? cmax(longest, 1) : split_shortest(longest, bs);
+}
+
+// The triples [x0, x1) of one CTA (none if x0 >= x1).  cuts: like prefix, in pieces of at most split_piece blocks.
+struct SplitRange {
+    long long x0, x1;
+    long long u;                   // not aligned: triples of every CTA
+    bool aligned;                  // pieces of whole groups: this CTA's group has `pieces`, from CTA `first` on
+    int first, pieces;
+};
+
+__host__ __device__ __forceinline__ SplitRange split_range(const int *prefix, const int *cuts, int num_seqs, int h_kv, int bs,
+                                                           int longest, int ctas, int cta)
+{
+    SplitRange r{0, 0, 0, (long long)cuts[num_seqs] * h_kv <= ctas, 0, 0};
+    if (r.aligned) {
+        if (cta < cuts[num_seqs] * h_kv) {
+            const SplitPlace at = split_locate(cuts, num_seqs, h_kv, cta);          // at.nb, at.block: pieces
+            const int nb = prefix[at.seq + 1] - prefix[at.seq], each = ceil_div(nb, at.nb);
+            const long long group0 = (long long)prefix[at.seq] * h_kv + (long long)at.kvh * nb;
+            r.first = cta - at.block;
+            r.pieces = ceil_div(nb, each);
+            r.x0 = group0 + cmin(nb, at.block * each);
+            r.x1 = group0 + cmin(nb, (at.block + 1) * each);
+        }
+    } else {
+        const long long total = (long long)prefix[num_seqs] * h_kv;
+        r.u = (total + ctas - 1) / ctas;
+        if (r.u < split_shortest(longest, bs)) r.u = split_shortest(longest, bs);
+        r.x0 = cta * r.u;
+        r.x1 = total < r.x0 + r.u ? total : r.x0 + r.u;
+    }
+    return r;
+}
+
+// The CTAs that share the group of triples [group0, group0 + nb): the first of them and how many; and which partial
+// slot CTA c of them leaves its part in (of its two: 0, or 1 for a group that begins inside its range).
+__host__ __device__ __forceinline__ void split_sharers(const SplitRange &r, long long group0, int nb, int &c0, int &pieces)
+{
+    c0 = r.aligned ? r.first : (int)(group0 / r.u);
+    pieces = r.aligned ? r.pieces : (int)((group0 + nb - 1) / r.u) - c0 + 1;
+}
+__host__ __device__ __forceinline__ int split_slot(const SplitRange &r, long long group0, int c)
+{
+    return 2 * c + (!r.aligned && group0 > c * r.u ? 1 : 0);
 }
 
 // Ext: struct with `kDependent` (a programmatic dependent launch follows), `Args` (kernel argument), `Row<G>` (built per group; its functions for bf16 only, see
@@ -339,7 +396,7 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, SplitConfi
         }
         __syncwarp();
         // cuts[s] = pieces of one KV head of the sequences before s
-        const int u_cut = most * BS <= kSplitWholeTokens ? max(most, 1) : max(kSplitMinTokens / BS, ceil_div(most, kSplitMaxPieces - 2));
+        const int u_cut = split_piece(most, BS);
         carry = 0;
         for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
             const int s = s0 + lane, n = s < p.num_seqs ? ceil_div(prefix[s + 1] - prefix[s], u_cut) : 0;
@@ -361,27 +418,8 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, SplitConfi
             for (int i = threadIdx.x; i < p.h_q * D / 8; i += SC::THREADS)
                 reinterpret_cast<uint4 *>(p.out + (size_t)s * p.h_q * D)[i] = make_uint4(0, 0, 0, 0);
 
-    const long long total = (long long)prefix[p.num_seqs] * p.h_kv;
-    const int u_min = max(kSplitMinTokens / BS, ceil_div(*longest, kSplitMaxPieces - 2));
-    // pieces of whole groups: this CTA's group and piece, if there are CTAs enough
-    const bool aligned = (long long)cuts[p.num_seqs] * p.h_kv <= gridDim.x;
-    long long u = 0, x0 = 0, x1 = 0;
-    int first_cta = 0, group_pieces = 0;                       // aligned: of this CTA's group
-    if (aligned) {
-        if ((int)blockIdx.x < cuts[p.num_seqs] * p.h_kv) {
-            const SplitPlace at = split_locate(cuts, p.num_seqs, p.h_kv, blockIdx.x);    // at.nb, at.block: pieces
-            const int nb = prefix[at.seq + 1] - prefix[at.seq], each = ceil_div(nb, at.nb);
-            const long long group0 = (long long)prefix[at.seq] * p.h_kv + (long long)at.kvh * nb;
-            first_cta = (int)blockIdx.x - at.block;
-            group_pieces = ceil_div(nb, each);
-            x0 = group0 + min(nb, at.block * each);
-            x1 = group0 + min(nb, (at.block + 1) * each);
-        }
-    } else {
-        u = max((total + gridDim.x - 1) / gridDim.x, (long long)u_min);
-        x0 = (long long)blockIdx.x * u;
-        x1 = min(total, x0 + u);
-    }
+    const SplitRange range = split_range(prefix, cuts, p.num_seqs, p.h_kv, BS, *longest, gridDim.x, blockIdx.x);
+    const long long x0 = range.x0, x1 = range.x1;
     if (x0 >= x1) return;                                      // uniform over the CTA
 
     if (warp == NW) {
@@ -567,7 +605,7 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, SplitConfi
         for (int w = 0; w < NW; ++w) failed = failed || bad_flag[w] != 0;
         const bool whole = at.block == 0 && n == at.nb;
         const long long group0 = x - n - at.block;                           // the group's first triple
-        const int slot = 2 * blockIdx.x + (!aligned && group0 > x0 ? 1 : 0);
+        const int slot = split_slot(range, group0, blockIdx.x);
         const float nan = __int_as_float(0x7fc00000);
         for (int idx = tid; idx < G * D / 4; idx += NW * 32) {
             const int h = idx / (D / 4), d4 = idx % (D / 4);
@@ -599,8 +637,8 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, SplitConfi
         // ---- count; the CTA that completes the group merges it ----
         // the barrier orders all partial writes before thread 0's fence and count (release); whoever sees
         // the count complete fences before its threads read the others' partials (acquire)
-        const int c0 = aligned ? first_cta : (int)(group0 / u);
-        const int pieces = aligned ? group_pieces : (int)((group0 + at.nb - 1) / u) - c0 + 1;
+        int c0, pieces;
+        split_sharers(range, group0, at.nb, c0, pieces);
         if (tid == 0) {
             int *cnt = p.counters + (size_t)at.seq * p.h_kv + at.kvh;
             __threadfence();
@@ -613,14 +651,13 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, SplitConfi
         }
         consumers_sync<NW>();
         if (!*last_flag) continue;
-        auto slot_of = [&](int c) { return 2 * c + (!aligned && group0 > (long long)c * u ? 1 : 0); };
         // a warp for each head, a lane for each piece (and the one 32 further): weights 2^(m - M) / L
         for (int h = warp; h < G; h += NW) {
             float2 ml[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int c = lane + 32 * i;
-                ml[i] = c < pieces ? __ldcg(reinterpret_cast<const float2 *>(p.part_ml) + (size_t)slot_of(c0 + c) * G + h)
+                ml[i] = c < pieces ? __ldcg(reinterpret_cast<const float2 *>(p.part_ml) + (size_t)split_slot(range, group0, c0 + c) * G + h)
                                    : make_float2(-INFINITY, 0.f);
             }
             float M = fmaxf(ml[0].x, ml[1].x);
@@ -645,7 +682,7 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, SplitConfi
 #pragma unroll
                 for (int i = 0; i < R; ++i)
                     if (q0 + i < pieces)
-                        v[i] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + ((size_t)slot_of(c0 + q0 + i) * G + h) * D) + d4);
+                        v[i] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + ((size_t)split_slot(range, group0, c0 + q0 + i) * G + h) * D) + d4);
 #pragma unroll
                 for (int i = 0; i < R; ++i)
                     if (q0 + i < pieces) {
