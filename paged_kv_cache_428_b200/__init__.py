@@ -496,12 +496,30 @@ def pa_reshape_and_cache_block_scales(key, value, k_cache, v_cache, k_scales, v_
                                       stream=None) -> None:
     """Write bf16 rows [T, h_kv, d] into 8-bit caches with one scale for each (block, KV head); the scales
     are kept by the call.  The tokens of one block stand next to each other in slot_mapping."""
-    if k_cache.dtype not in QUANT_DTYPES:
-        raise TypeError("k_cache: dtype %s, expected one of %s" % (k_cache.dtype, QUANT_DTYPES))
-    r = reshape_call_args(key, value, k_cache, v_cache, slot_mapping)
-    _need_scales(k_scales, v_scales, r[11], r[8])
+    bf16, f32 = torch.bfloat16, torch.float32
+    try:                                       # everything at once; what is wrong is found out below
+        T, h_kv, d = size = key.shape
+        pool, cache, ks, vs = k_cache.shape, k_cache.dtype, key.stride(), value.stride()
+        NB, _, bs, _ = pool
+        fine = (key.dtype is bf16 and value.dtype is bf16 and value.shape == size and ks[2] == 1 and ks[1] == d
+                and vs[2] == 1 and vs[1] == d and (T < 2 or (ks[0] > 0 and vs[0] > 0))
+                and cache in QUANT_DTYPES and v_cache.dtype is cache
+                and pool[1] == h_kv and pool[3] == d and v_cache.shape == pool and k_scales.dtype is f32
+                and v_scales.dtype is f32 and k_scales.shape == (NB, h_kv) and v_scales.shape == (NB, h_kv)
+                and slot_mapping.dtype is torch.int64 and slot_mapping.shape == (T,) and key.is_cuda
+                and k_cache.is_contiguous() and v_cache.is_contiguous() and k_scales.is_contiguous()
+                and v_scales.is_contiguous() and slot_mapping.is_contiguous())
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine:
+        if k_cache.dtype not in QUANT_DTYPES:
+            raise TypeError("k_cache: dtype %s, expected one of %s" % (k_cache.dtype, QUANT_DTYPES))
+        r = reshape_call_args(key, value, k_cache, v_cache, slot_mapping)
+        _need_scales(k_scales, v_scales, r[11], r[8])
+        raise ValueError("rows, caches, scales and slot_mapping do not fit together")
     _check(_lib.pa_reshape_and_cache_block_scales(
-        *r[:6], k_scales.data_ptr(), v_scales.data_ptr(), *r[6:13],
+        key.data_ptr(), value.data_ptr(), ks[0] if T > 1 else 0, vs[0] if T > 1 else 0, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
+        v_scales.data_ptr(), slot_mapping.data_ptr(), T, h_kv, d, bs, NB, cache_dtype_code(k_cache),
         _on_current_device(stream, key, value, k_cache, v_cache, k_scales, v_scales, slot_mapping)),
         "pa_reshape_and_cache_block_scales")
 
@@ -538,25 +556,24 @@ def pa_decode_block_scales_workspace_size(num_seqs: int, h_q: int, h_kv: int, he
     return int(_lib.pa_decode_block_scales_workspace_size(num_seqs, h_q, h_kv, head_dim, max_context_len))
 
 
-def _split_workspace(workspace, size: int, device) -> torch.Tensor:
-    """The caller's workspace, or a new zero-filled one of `size` bytes."""
-    if workspace is None:
-        return torch.zeros(max(size, 16), dtype=torch.uint8, device=device)
-    _need(workspace, "workspace", (torch.uint8,), 1)
-    return workspace
+def _new_workspace(size: int, q: torch.Tensor) -> torch.Tensor:
+    """A zero-filled workspace of `size` bytes where q is."""
+    return torch.zeros(max(size, 16), dtype=torch.uint8, device=q.device)
 
 
 def _need_decode(out, q, k_cache, v_cache, block_tables, context_lens, dtypes) -> tuple:
     """Checks of the split decodes; (num_seqs, h_q, head_dim, num_blocks, h_kv, block_size)."""
     bf16, i32 = torch.bfloat16, torch.int32
     try:                                       # everything at once; what is wrong is found out below
-        size, pool = q.shape, k_cache.shape
-        fine = (q.dtype is bf16 and out.dtype is bf16 and k_cache.dtype in dtypes and v_cache.dtype is k_cache.dtype
-                and block_tables.dtype is i32 and context_lens.dtype is i32 and len(size) == 3 and len(pool) == 4
-                and block_tables.dim() == 2 and context_lens.dim() == 1 and q.is_cuda and q.is_contiguous()
-                and out.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
-                and block_tables.is_contiguous() and context_lens.is_contiguous())
-    except AttributeError:
+        size, pool, cache = q.shape, k_cache.shape, k_cache.dtype
+        B, h_q, d = size
+        NB, h_kv, bs, d2 = pool
+        rows, (count,) = block_tables.shape, context_lens.shape
+        fine = (q.dtype is bf16 and out.dtype is bf16 and cache in dtypes and v_cache.dtype is cache
+                and block_tables.dtype is i32 and context_lens.dtype is i32 and len(rows) == 2 and q.is_cuda
+                and q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous()
+                and v_cache.is_contiguous() and block_tables.is_contiguous() and context_lens.is_contiguous())
+    except (AttributeError, ValueError):
         fine = False
     if not fine:
         _need(out, "out", (bf16,), 3)
@@ -565,10 +582,10 @@ def _need_decode(out, q, k_cache, v_cache, block_tables, context_lens, dtypes) -
         _need(v_cache, "v_cache", (k_cache.dtype,), 4)
         _need(block_tables, "block_tables", (i32,), 2)
         _need(context_lens, "context_lens", (i32,), 1)
-    if out.shape != size or pool[3] != size[2] or v_cache.shape != pool or len(block_tables) != size[0] \
-            or len(context_lens) != size[0]:
+        raise ValueError("out, q, caches, block_tables and context_lens do not fit together")
+    if out.shape != size or d2 != d or v_cache.shape != pool or rows[0] != B or count != B:
         raise ValueError("shape mismatch between out, q, caches, block_tables and context_lens")
-    return *size, *pool[:3]
+    return B, h_q, d, NB, h_kv, bs
 
 
 def pa_decode_block_scales(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
@@ -577,8 +594,10 @@ def pa_decode_block_scales(out, q, k_cache, v_cache, k_scales, v_scales, block_t
     """pa_decode over an 8-bit cache with one scale for each (block, KV head); returns out."""
     B, h_q, d, NB, h_kv, bs = _need_decode(out, q, k_cache, v_cache, block_tables, context_lens, QUANT_DTYPES)
     _need_scales(k_scales, v_scales, NB, h_kv)
-    ws = _split_workspace(workspace, 0 if workspace is not None else pa_decode_block_scales_workspace_size(
-        B, h_q, h_kv, d, max_context_len), q.device)
+    ws = workspace
+    if ws is None:
+        ws = _new_workspace(pa_decode_block_scales_workspace_size(B, h_q, h_kv, d, max_context_len), q)
+    _need(ws, "workspace", (torch.uint8,), 1)
     _check(_lib.pa_decode_block_scales(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
         block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, int(max_context_len), h_q, h_kv, d, bs,
@@ -618,8 +637,10 @@ def pa_decode_scoremod(out, q, k_cache, v_cache, block_tables, context_lens, max
     the last `window` tokens; each is off by default.  Returns out."""
     B, h_q, d, NB, h_kv, bs = _need_decode(out, q, k_cache, v_cache, block_tables, context_lens, CACHE_DTYPES)
     window = _window(window)
-    ws = _split_workspace(workspace, 0 if workspace is not None else pa_decode_scoremod_workspace_size(
-        B, h_q, h_kv, d, max_context_len, window), q.device)
+    ws = workspace
+    if ws is None:
+        ws = _new_workspace(pa_decode_scoremod_workspace_size(B, h_q, h_kv, d, max_context_len, window), q)
+    _need(ws, "workspace", (torch.uint8,), 1)
     _check(_lib.pa_decode_scoremod(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         block_tables.shape[1], context_lens.data_ptr(), B, int(max_context_len), h_q, h_kv, d, bs, NB,
@@ -663,8 +684,10 @@ def pa_decode_weights(out, weights, q, k_cache, v_cache, block_tables, context_l
     _need(weights, "weights", (torch.float32,), 3)
     if weights.shape[0] != B or weights.shape[1] != h_kv:
         raise ValueError("weights must be [%d, %d, n], got %s" % (B, h_kv, tuple(weights.shape)))
-    ws = _split_workspace(workspace, 0 if workspace is not None else pa_decode_weights_workspace_size(
-        B, h_q, h_kv, d, max_context_len), q.device)
+    ws = workspace
+    if ws is None:
+        ws = _new_workspace(pa_decode_weights_workspace_size(B, h_q, h_kv, d, max_context_len), q)
+    _need(ws, "workspace", (torch.uint8,), 1)
     _check(_lib.pa_decode_weights(
         out.data_ptr(), weights.data_ptr(), weights.shape[2], q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
         block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, int(max_context_len), h_q, h_kv, d, bs,
@@ -679,26 +702,41 @@ def pa_evict(k_cache, v_cache, weights, block_tables, context_lens, new_block_ta
     """Keep at most `budget` tokens of every sequence: the last `recent` and the heaviest of the others, chosen
     per KV head, their rows copied in order to the blocks of new_block_tables.  Fills kept int32 [B, h_kv, budget],
     new_weights fp32 [B, h_kv, >= budget] and new_context_lens int32 [B]."""
-    _need(k_cache, "k_cache", CACHE_DTYPES, 4)
-    _need(v_cache, "v_cache", (k_cache.dtype,), 4)
-    _need(weights, "weights", (torch.float32,), 3)
-    _need(new_weights, "new_weights", (torch.float32,), 3)
-    _need(kept, "kept", (torch.int32,), 3)
-    _need(block_tables, "block_tables", (torch.int32,), 2)
-    _need(new_block_tables, "new_block_tables", (torch.int32,), 2)
-    _need(context_lens, "context_lens", (torch.int32,), 1)
-    _need(new_context_lens, "new_context_lens", (torch.int32,), 1)
-    NB, h_kv, bs, d = k_cache.shape
-    B = context_lens.shape[0]
-    if v_cache.shape != k_cache.shape or block_tables.shape[0] != B or new_block_tables.shape[0] != B \
-            or new_context_lens.shape[0] != B or tuple(kept.shape) != (B, h_kv, budget) \
-            or tuple(weights.shape[:2]) != (B, h_kv) or tuple(new_weights.shape[:2]) != (B, h_kv):
+    i32, f32 = torch.int32, torch.float32
+    try:                                       # everything at once; what is wrong is found out below
+        pool, cache = k_cache.shape, k_cache.dtype
+        NB, h_kv, bs, d = pool
+        B, = context_lens.shape
+        (rows, blocks), (new_rows, new_blocks) = block_tables.shape, new_block_tables.shape
+        (b1, h1, stride), (b2, h2, new_stride) = weights.shape, new_weights.shape
+        fine = (cache in CACHE_DTYPES and v_cache.dtype is cache and weights.dtype is f32 and new_weights.dtype is f32
+                and kept.dtype is i32 and block_tables.dtype is i32 and new_block_tables.dtype is i32
+                and context_lens.dtype is i32 and new_context_lens.dtype is i32 and k_cache.is_cuda
+                and k_cache.is_contiguous() and v_cache.is_contiguous() and weights.is_contiguous()
+                and new_weights.is_contiguous() and kept.is_contiguous() and block_tables.is_contiguous()
+                and new_block_tables.is_contiguous() and context_lens.is_contiguous()
+                and new_context_lens.is_contiguous())
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine:
+        _need(k_cache, "k_cache", CACHE_DTYPES, 4)
+        _need(v_cache, "v_cache", (k_cache.dtype,), 4)
+        _need(weights, "weights", (f32,), 3)
+        _need(new_weights, "new_weights", (f32,), 3)
+        _need(kept, "kept", (i32,), 3)
+        _need(block_tables, "block_tables", (i32,), 2)
+        _need(new_block_tables, "new_block_tables", (i32,), 2)
+        _need(context_lens, "context_lens", (i32,), 1)
+        _need(new_context_lens, "new_context_lens", (i32,), 1)
+        raise ValueError("caches, tables, lengths, weights and kept do not fit together")
+    if v_cache.shape != pool or rows != B or new_rows != B or new_context_lens.shape != (B,) \
+            or kept.shape != (B, h_kv, budget) or b1 != B or b2 != B or h1 != h_kv or h2 != h_kv:
         raise ValueError("shape mismatch between caches, tables, lengths, weights and kept")
     _check(_lib.pa_evict(
-        k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), weights.shape[2], block_tables.data_ptr(),
-        block_tables.shape[1], context_lens.data_ptr(), new_block_tables.data_ptr(), new_block_tables.shape[1], B,
-        int(max_context_len), int(budget), int(recent), h_kv, d, bs, NB, cache_dtype_code(k_cache), kept.data_ptr(),
-        new_weights.data_ptr(), new_weights.shape[2], new_context_lens.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), stride, block_tables.data_ptr(), blocks,
+        context_lens.data_ptr(), new_block_tables.data_ptr(), new_blocks, B, int(max_context_len), int(budget), int(recent),
+        h_kv, d, bs, NB, cache_dtype_code(k_cache), kept.data_ptr(), new_weights.data_ptr(), new_stride,
+        new_context_lens.data_ptr(),
         _on_current_device(stream, k_cache, v_cache, weights, block_tables, context_lens, new_block_tables, kept, new_weights,
                            new_context_lens)), "pa_evict")
 

@@ -173,7 +173,10 @@ def test_write_strided_rows_and_no_rows():
     qkv = torch.randn((20, 4 * h, d), generator=g).to(torch.bfloat16).to(DEV)
     c.write(qkv[:, h:2 * h], qkv[:, 3 * h:], list(range(20)))
     c.write(qkv[:0, :h], qkv[:0, :h], [])
+    c.write(qkv[3:4, :h].as_strided((1, h, d), (1, d, 1), qkv.storage_offset()), qkv[4:5, h:2 * h], [33])   # one row: any stride
     c.check()
+    with pytest.raises(ValueError):              # rows on top of each other: a stride of 0 would mean packed rows
+        c.write(qkv[:1, :h].expand(3, h, d), qkv[:3, :h].contiguous(), [0, 1, 2])
 
 
 def test_copy_scales_with_the_blocks():
