@@ -657,15 +657,35 @@ def pa_prefill_scoremod(out, q, k_cache, v_cache, block_tables, query_start, con
                         stream=None) -> torch.Tensor:
     """pa_prefill_ws with modified scores (see pa_decode_scoremod); tokens before prefix_lens[s] (int32 [B]) are
     seen by all rows of sequence s.  workspace: make_prefill_workspace().  Returns out."""
-    a = prefill_call_args(out, q, k_cache, v_cache, block_tables, query_start, context_lens, max_query_len, scale)
+    bf16, i32 = torch.bfloat16, torch.int32
+    try:                                       # everything at once; what is wrong is found out below
+        size, pool, cache = q.shape, k_cache.shape, k_cache.dtype
+        _, h_q, d = size
+        NB, h_kv, bs, d2 = pool
+        (rows, blocks), (B,), (starts,) = block_tables.shape, context_lens.shape, query_start.shape
+        fine = (q.dtype is bf16 and out.dtype is bf16 and cache in CACHE_DTYPES and v_cache.dtype is cache
+                and block_tables.dtype is i32 and context_lens.dtype is i32 and query_start.dtype is i32 and q.is_cuda
+                and out.shape == size and d2 == d and v_cache.shape == pool and rows == B and starts == B + 1
+                and q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous()
+                and v_cache.is_contiguous() and block_tables.is_contiguous() and context_lens.is_contiguous()
+                and query_start.is_contiguous())
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine:
+        prefill_call_args(out, q, k_cache, v_cache, block_tables, query_start, context_lens, max_query_len, scale)
+        raise ValueError("out, q, caches, block_tables, query_start and context_lens do not fit together")
     _need(workspace, "workspace", (torch.uint8,), 1)
+    prefix = None
     if prefix_lens is not None:
-        _need(prefix_lens, "prefix_lens", (torch.int32,), 1)
-        if prefix_lens.shape[0] != context_lens.shape[0]:
-            raise ValueError("prefix_lens: expected %d, got %d" % (context_lens.shape[0], prefix_lens.shape[0]))
+        _need(prefix_lens, "prefix_lens", (i32,), 1)
+        if prefix_lens.shape[0] != B:
+            raise ValueError("prefix_lens: expected %d, got %d" % (B, prefix_lens.shape[0]))
+        prefix = prefix_lens.data_ptr()
     _check(_lib.pa_prefill_scoremod(
-        *a[:16], float(softcap), _slopes_ptr(alibi_slopes, q.shape[1]), _window(window),
-        None if prefix_lens is None else prefix_lens.data_ptr(), a[16], workspace.data_ptr(), workspace.numel(),
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), blocks,
+        query_start.data_ptr(), context_lens.data_ptr(), B, int(max_query_len), h_q, h_kv, d, bs, NB,
+        1.0 / math.sqrt(d) if scale is None else float(scale), float(softcap), _slopes_ptr(alibi_slopes, h_q),
+        _window(window), prefix, cache_dtype_code(k_cache), workspace.data_ptr(), workspace.numel(),
         _on_current_device(stream, out, q, k_cache, v_cache, block_tables, query_start, context_lens, alibi_slopes,
                            prefix_lens, workspace)), "pa_prefill_scoremod")
     return out

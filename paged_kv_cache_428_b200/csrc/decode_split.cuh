@@ -24,6 +24,10 @@
 // begins in, 1: the one it ends in) and counts; the CTA that completes the count merges.  No CTA waits
 // for another, and the merge adds in the order of the CTAs: results do not depend on timing.
 //
+// Bound by the bytes of K and V: 64 sequences of 512..4096 tokens (613 MB) 100 to 104 us, 32 x 4096 tokens of 32 heads
+// in E4M3 (1076 MB) 178 to 188 us, 91 to 94 and 88 to 93 % of the copy rate.  Single short sequences are bound by
+// latency: 5.8 us for 2 x 37..81 tokens, of which three dependent loads (length, table, tiles) are about 2.
+//
 // Masked places.  Scores of tokens outside [first, ctx) become -inf by select, V rows there are
 // zeroed (in shared memory for bf16, in registers for codes): what they hold does not matter.
 #pragma once

@@ -24,7 +24,8 @@ __device__ __forceinline__ float rcp_approx(float x)
 
 // The softmax warps bound the prefill kernel, and their registers are full: what is done to a score there
 // counts, and so does every branch around it.  Hence four kernels, by whether scores are capped and biased:
-//   window, prefix     only the tiles at the borders are masked; scores stay as they are.
+//   window, prefix     only the tiles at the borders are masked; scores stay as they are.  (8 chunks of 512
+//                      after 0..3584 tokens, 32 heads of 128: 166 us, 164 without either; CAP 193; BIAS 193.)
 //   BIAS               one multiply-add to the raw score, slope / scale times the place in the tile; what the
 //                      whole tile has in common goes into the softmax's reference.  Only tiles with tokens on
 //                      both sides of a row need more.
