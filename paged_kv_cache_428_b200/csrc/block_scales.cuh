@@ -2,11 +2,11 @@
 // the write that keeps the scales, and what the decode of decode_split.cuh needs to know.
 //
 // The scale of a block is the smallest bf16 number s with QMAX s >= max|x| over the block's rows (QMAX = 448
-// for E4M3, 127 for INT8), but at least 2^-80 unless all of them are 0, kept in fp32.  A code is x / s to nearest, ties to even.  With 8 significant
-// bits in x and in s, and at most 7 in a code, x / s and code * s_old / s_new round in fp32 exactly as in
-// any wider type (a quotient of such numbers that is not a tie is further from one than 2^-17 of it):
-// codes are what the definition says, bit for bit.  Against max|x| / QMAX itself the scale is at most 2^-7
-// larger.
+// for E4M3, 127 for INT8), but at least 2^-80 unless all of them are 0, kept in fp32.  A code is x / s to nearest,
+// ties to even.  With 8 significant bits in x and in s, and at most 7 in a code, x / s and code * s_old / s_new
+// round in fp32 exactly as in any wider type (a quotient of such numbers that is not a tie is further from one than
+// 2^-17 of it): codes are what the definition says, bit for bit.  Against max|x| / QMAX itself the scale is at
+// most 2^-7 larger.
 //
 // Bound by: latency for a decode step's rows; the rows' bytes in and codes out for prompts.
 #pragma once
@@ -67,8 +67,8 @@ __device__ __forceinline__ uint32_t encode4(float x0, float x1, float x2, float 
 // one residual step (as in Markstein's division), q1 = q0 + (x - q0 s) r.  The residual is exact, so q1 is
 // within a step of the quotient, and is the quotient where that is an fp32 number.  Ties between two codes are
 // fp32 numbers, and every other quotient of 8-bit significands is further than that from a tie: the codes
-// are those of the division, at 3 packed instructions for two values instead of about 24.  INT8: |q| <= 127 by the choice of the scale, and adding
-// 1.5 * 2^23 rounds it to nearest, ties to even, into the low byte.
+// are those of the division, at 3 packed instructions for two values instead of about 24.  INT8: |q| <= 127 by the
+// choice of the scale, and adding 1.5 * 2^23 rounds it to nearest, ties to even, into the low byte.
 template <int QT>
 __device__ __forceinline__ uint32_t encode4_fast(float x0, float x1, float x2, float x3, float s, float r)
 {

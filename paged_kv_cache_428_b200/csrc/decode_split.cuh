@@ -85,7 +85,8 @@ struct SplitConfig {
     static constexpr int THREADS = Tile::THREADS;
     static constexpr int STAGES = Tile::STAGES;
     // blocks that the producer issues together, a lane each: half the ring (a power of two)
-    static constexpr int kIssue = STAGES >= 64 ? 32 : STAGES >= 32 ? 16 : STAGES >= 16 ? 8 : STAGES >= 8 ? 4 : STAGES >= 4 ? 2 : 1;
+    static constexpr int kIssue =
+        STAGES >= 64 ? 32 : STAGES >= 32 ? 16 : STAGES >= 16 ? 8 : STAGES >= 8 ? 4 : STAGES >= 4 ? 2 : 1;
     static constexpr int OFF_BARS = Tile::RING;
     static constexpr int OFF_STAGE = OFF_BARS + 2 * STAGES * 8;
     static constexpr int OFF_FLAGS = OFF_STAGE + STAGES * (int)sizeof(SplitStage);   // abort, last, longest, bad[NW]
@@ -341,8 +342,9 @@ __host__ __device__ __forceinline__ int split_slot(const SplitRange &r, long lon
     return 2 * c + (!r.aligned && group0 > c * r.u ? 1 : 0);
 }
 
-// Ext: struct with `kDependent` (a programmatic dependent launch follows), `Args` (kernel argument), `Row<G>` (built per group; its functions for bf16 only, see
-// split_consume_bf16) and, for codes, k_scales / v_scales [num_blocks][h_kv] in Args.
+// Ext: struct with `kDependent` (a programmatic dependent launch follows), `Args` (kernel argument), `Row<G>` (built
+// per group; its functions for bf16 only, see split_consume_bf16) and, for codes, k_scales / v_scales
+// [num_blocks][h_kv] in Args.
 template <int D, int BS, int G, int QT, class Ext>
 __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, SplitConfig<D, BS, G, QT>::kPerSm)
     paged_decode_split_kernel(const SplitParams p, const typename Ext::Args args,
@@ -661,7 +663,8 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, SplitConfi
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int c = lane + 32 * i;
-                ml[i] = c < pieces ? __ldcg(reinterpret_cast<const float2 *>(p.part_ml) + (size_t)split_slot(range, group0, c0 + c) * G + h)
+                const float2 *from = reinterpret_cast<const float2 *>(p.part_ml);
+                ml[i] = c < pieces ? __ldcg(from + (size_t)split_slot(range, group0, c0 + c) * G + h)
                                    : make_float2(-INFINITY, 0.f);
             }
             float M = fmaxf(ml[0].x, ml[1].x);
@@ -686,7 +689,8 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, SplitConfi
 #pragma unroll
                 for (int i = 0; i < R; ++i)
                     if (q0 + i < pieces)
-                        v[i] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + ((size_t)split_slot(range, group0, c0 + q0 + i) * G + h) * D) + d4);
+                        v[i] = __ldcg(reinterpret_cast<const float4 *>(p.part_o) +
+                                      ((size_t)split_slot(range, group0, c0 + q0 + i) * G + h) * (D / 4) + d4);
 #pragma unroll
                 for (int i = 0; i < R; ++i)
                     if (q0 + i < pieces) {

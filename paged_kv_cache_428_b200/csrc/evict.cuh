@@ -63,8 +63,8 @@ struct AddWeightsParams {
 constexpr int kAddThreads = 128, kAddPer = 4;          // threads, tokens of each
 
 // grid (ceil(max_tokens / (threads * per)), h_kv, B).  Bound by latency (length, denominators and logits, 28 MB mostly
-// from L2): 8.7 us for 64 sequences of 512..4096 tokens and 8 KV heads, partly behind the decode's end.  A sequence whose denominator is not finite (a block outside
-// the pool, NaN among its values) keeps its weights.
+// from L2): 8.7 us for 64 sequences of 512..4096 tokens and 8 KV heads, partly behind the decode's end.  A sequence
+// whose denominator is not finite (a block outside the pool, NaN among its values) keeps its weights.
 template <int G>
 __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const AddWeightsParams p)
 {
