@@ -25,7 +25,7 @@
 // for another, and the merge adds in the order of the CTAs: results do not depend on timing.
 //
 // Bound by the bytes of K and V: 64 sequences of 512..4096 tokens (613 MB) 100 to 104 us, 32 x 4096 tokens of 32 heads
-// in E4M3 (1076 MB) 178 to 188 us, 91 to 94 and 88 to 93 % of the copy rate.  Single short sequences are bound by
+// in E4M3 (1076 MB) 176 to 188 us, 91 to 94 and 88 to 93 % of the copy rate.  Single short sequences are bound by
 // latency: 5.8 us for 2 x 37..81 tokens, of which three dependent loads (length, table, tiles) are about 2.
 //
 // Masked places.  Scores of tokens outside [first, ctx) become -inf by select, V rows there are
@@ -210,6 +210,37 @@ __device__ __forceinline__ void split_consume_bf16(uint8_t *ktile, int lo, int h
             mma_bf16_16816(st.o[mt], a[0], a[1], a[2], a[3], pb0, pb1);
         }
     }
+}
+
+// Q^T fragments in fp16, in the order of q8_load_q: the group's q is brought by a power of two to a largest
+// magnitude in [2^13, 2^14), so that neither large nor small queries leave fp16's normal range; returns what
+// the logits have to be multiplied by for it.  (q8_load_q only brings large ones down: queries near 2^-14 beside
+// large keys would lose digits there.)
+template <class C, int G, int D>
+__device__ __forceinline__ float split_load_q8(uint32_t (&qb)[C::KS][2], const __nv_bfloat16 *qg, int lane)
+{
+    const int gq = lane >> 2, tq = lane & 3;
+    const __nv_bfloat16 *qrow = qg + (size_t)(gq < G ? gq : 0) * D;
+    uint2 raw[C::KS];
+    float mx = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < C::KS; ++ks) {
+        raw[ks] = gq < G ? *reinterpret_cast<const uint2 *>(qrow + 16 * ks + 4 * tq) : make_uint2(0u, 0u);
+        const float2 a = bf16x2_to_float2(raw[ks].x), b = bf16x2_to_float2(raw[ks].y);
+        mx = fmaxf(mx, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y))));
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    // the exponent of mx less 13, kept where both powers of two are normal numbers
+    const int e = max(-100, min(114, (int)(__float_as_uint(mx) >> 23) - 127 - 13));
+    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+    for (int ks = 0; ks < C::KS; ++ks) {
+        const float2 a = bf16x2_to_float2(raw[ks].x), b = bf16x2_to_float2(raw[ks].y);
+        qb[ks][0] = pack_f16x2(a.x * down, a.y * down);
+        qb[ks][1] = pack_f16x2(b.x * down, b.y * down);
+    }
+    return __uint_as_float((uint32_t)(127 + e) << 23);
 }
 
 // One block of codes into the state.  The block's scales enter the logit: x = dot * k_factor + log2(v),
@@ -538,7 +569,7 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, SplitConfi
         if constexpr (QT == 0) {
             mma_load_q<C, G, D>(qb, p.q + head0 * D, lane);
         } else {
-            k_factor *= q8_load_q<C, G, D>(qb, p.q + head0 * D, lane);
+            k_factor *= split_load_q8<C, G, D>(qb, p.q + head0 * D, lane);
             q8_k_bias<C, QT>(qb, lane, kbias);
         }
         SplitState<MT> state;

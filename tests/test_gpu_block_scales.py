@@ -282,6 +282,17 @@ def test_decode_scales_far_apart(kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("power", [-60, -20, 40])
+def test_decode_queries_of_any_size(kind, power):
+    """Tiny queries over large keys and the other way round: the logits are ordinary."""
+    q, codes, scales, tab, ctx = _decode_case(kind, 64, 16, 4, [90, 17], seed=21, spread=0.3)
+    q = (q.float() * 2.0 ** power).to(torch.bfloat16)
+    q[:, 1] = 0.0
+    scales[0] *= 2.0 ** -power
+    _check((q, codes, scales, tab, ctx), _run((q, codes, scales, tab, ctx)))
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("lens,h_kv,g,d,bs", [
     ([70001], 1, 4, 64, 16),                    # one group, as many pieces as there can be
     ([33000, 5], 2, 1, 128, 64),
