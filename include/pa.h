@@ -414,8 +414,9 @@ int pa_validate_block_runs(const int64_t *slot_mapping, int num_tokens, int bloc
 
 /* pa_decode over such a cache.  Same result as pa_decode over the values code * scale: fp32 sums,
  * probabilities rounded to fp16 (2^-11) for the product with the codes, relative to the largest
- * probability * V scale, so that blocks with very different scales add up without loss.  V scales are
- * finite and at least 2^-80, or 0 (a block whose codes are all 0), as the write leaves them.
+ * probability * V scale, so that blocks with very different scales add up without loss: what is below 2^-29
+ * of the largest such product loses digits.  V scales are finite and at least 2^-80, or 0 (a block whose
+ * codes are all 0; it counts as 2^-80 there), as the write leaves them.
  *   max_context_len  host-known bound of context_lens; it only sizes the grid
  *   workspace      device, >= pa_decode_block_scales_workspace_size(...) bytes, 16-byte aligned, zero before
  *                  its first use; every call leaves it ready for the next one, of whatever sizes, here

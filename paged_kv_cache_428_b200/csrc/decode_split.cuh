@@ -492,8 +492,9 @@ __global__ void __launch_bounds__(SplitConfig<D, BS, G, QT>::THREADS, SplitConfi
             if (i0 + 32 < n) look(i0 + 32 + lane, row_n, ks_n, vs_n);
             float v_log2 = 0.f, v_inv = 1.f;
             if constexpr (QT != 0) {
-                // a block whose V codes are all 0 has scale 0: any scale stands for it
-                const float v = vs > 0.f ? fmaxf(vs, kMinBlockScale) : 1.f;
+                // a block whose V codes are all 0 has scale 0; it counts as the smallest scale there is, as it must not
+                // set the reference that the other blocks' probabilities are held to (see split_consume_q8)
+                const float v = fmaxf(vs, kMinBlockScale);
                 v_log2 = log2f(v);
                 v_inv = 1.f / v;
             }

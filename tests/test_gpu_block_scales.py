@@ -282,6 +282,39 @@ def test_decode_scales_far_apart(kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("power", [-20, -34, -44, -60, -80])
+def test_decode_zero_blocks_beside_small_scales(kind, power):
+    """Blocks with V scale 0 (all their rows were 0) beside blocks whose V scales are as small as the write leaves
+    them: the others' share of the output keeps its digits, a sequence of nothing else gives 0."""
+    q, codes, scales, tab, ctx = _decode_case(kind, 128, 16, 4, [400, 90, 40], seed=31, spread=0.0)
+    scales[0].fill_(0.002)
+    scales[1].fill_(2.0 ** power)
+    zero = torch.cat([tab[0, 1:25:3], tab[1, 2:4], tab[2, :3]]).long()
+    scales[1][zero] = 0.0
+    codes[1].view(torch.uint8)[zero] = 0
+    case = (q, codes, scales, tab, ctx)
+    out = _run(case)
+    _check(case, out)
+    assert not out[2].any()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_zero_rows_written_beside_tiny_ones(kind):
+    """The same through the write: a block of zero V rows, then blocks of tiny ones."""
+    g, h, d, bs = _gen(32), 2, 64, 16
+    c = Cache(9, h, bs, d, kind)
+    order = [3, 1, 5, 0, 8, 2, 7]
+    k, v = _rows(112, h, d, g), _rows(112, h, d, g) * 2.0 ** -45
+    v[:16] = 0
+    c.write(k, v, _slots(order, 0, 112, bs))
+    c.check()
+    q = (torch.randn((1, 4 * h, d), generator=g) * 0.5).to(torch.bfloat16)
+    case = (q, (c.k.cpu(), c.v.cpu()), (c.ks.cpu(), c.vs.cpu()), torch.tensor([order], dtype=torch.int32),
+            torch.tensor([105], dtype=torch.int32))
+    _check(case, _run(case))
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("power", [-60, -20, 40])
 def test_decode_queries_of_any_size(kind, power):
     """Tiny queries over large keys and the other way round: the logits are ordinary."""
