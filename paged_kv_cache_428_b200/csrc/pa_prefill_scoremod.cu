@@ -42,7 +42,12 @@ int dispatch_scoremod(int d, int bs, int g, const PrefillParams &pp, int n, int 
         mod.cap_out = (float)to;
         mod.range = (float)(PA_TANH_RANGE / in);
         double f = to * in;
-        for (int i = 0; i < 3; ++i, f *= in * in) mod.c[i] = (float)(coef[i] * f);
+        for (int i = 0; i < 3; ++i, f *= in * in) {
+            mod.c[i] = (float)(coef[i] * f);
+            // (scale / cap)^5 cap can pass fp32, and 0 times that is NaN: caps that small (1e-11 at a scale of 1 / 8) go
+            // without the polynomial
+            if (!std::isfinite(mod.c[i])) mod.range = -1.f;
+        }
     }
     return d == 64 ? dispatch_scoremod_block<64>(bs, g, pp, n, mql, counters, mod, st)
                    : dispatch_scoremod_block<128>(bs, g, pp, n, mql, counters, mod, st);

@@ -161,6 +161,13 @@ def test_caps_far_from_the_scores(softcap):
     _prefill([60, 0], [80, 30], 2, 4, 16, 64, 14, softcap=softcap)
 
 
+@pytest.mark.parametrize("softcap", [2.0 ** -64, 1e-15, 1e-11, 1e-6, 50.0, 1e25, 2e38])
+def test_scores_that_are_all_zero(softcap):
+    """Zero queries (as in padded rows) under caps of any size: plain means of V."""
+    _decode([200, 33], 2, 4, 16, 64, 24, softcap=softcap, q_factor=0.0)
+    _prefill([60, 0], [80, 30], 2, 4, 16, 64, 24, softcap=softcap, q_factor=0.0)
+
+
 def test_decode_without_any_is_decode():
     gen = _gen(5)
     k, v, tab, _ = _pool([400, 77], 2, 16, 128, gen)
