@@ -339,14 +339,14 @@ int pa_validate_slots(const int64_t *slot_mapping, int num_tokens, int block_siz
  * scores before the softmax.  With p the position of the query row (context_lens[s] - 1 for a decode
  * step) and t that of the key, in this order:
  *   x = scale * q . k
- *   softcap > 0:    x = softcap * tanh(x / softcap)      (0 = no cap; else at least 2^-64 and finite, or
- *                   PA_ERR_INVALID_ARG)
+ *   softcap > 0:    x = softcap * tanh(x / softcap)      (0 = no cap; else at least 2^-64)
  *   alibi_slopes:   x = x - alibi_slopes[h] * |p - t|    (device fp32 [h_q], finite; NULL = no bias)
  *   window > 0:     only tokens t > p - window are seen, the query's own among them (0 = no window)
  *   prefix_lens:    tokens t < prefix_lens[s] are seen by every row of sequence s (inside its window),
  *                   also those behind it (device int32 [num_seqs], at most context_lens[s] count; NULL =
  *                   causal).  Prefill only: a decode step sees no token behind it.
- * and out = softmax(x) . V over the tokens seen.  Documents that must not see each other are sequences of
+ * scale, softcap and 2 scale / softcap, each times log2(e), are finite in fp32 (else PA_ERR_INVALID_ARG).
+ * And out = softmax(x) . V over the tokens seen.  Documents that must not see each other are sequences of
  * their own here (a row of block_tables and a stretch of query_start each), which is what a document mask
  * says.
  * Blocks that lie before the window of every row of the call are not read: their table entries need not be

@@ -215,8 +215,13 @@ int collect_device_errors(unsigned int *flags, int clear)
     return PA_OK;
 }
 
-// tanh cap of the scores: 0 = none (below 2^-64 its inverse times a score would leave fp32).
-bool valid_softcap(float cap) { return std::isfinite(cap) && (cap == 0.f || cap >= 0x1p-64f); }
+// Scores are multiplied by scale * log2(e), and by 2 / cap more inside the tanh, and come out as cap * log2(e): all
+// of these have to be numbers in fp32 (infinity times a score of 0 is NaN).  cap: 0 = none, else at least 2^-64.
+bool valid_scores(float scale, float cap)
+{
+    if (!std::isfinite(scale * kLog2e) || !std::isfinite(cap * kLog2e) || !(cap == 0.f || cap >= 0x1p-64f)) return false;
+    return cap == 0.f || std::isfinite(2.f * (scale * kLog2e) / cap);
+}
 
 }  // namespace
 

@@ -40,7 +40,7 @@ int dispatch_scoremod(int d, int bs, int g, const PrefillParams &pp, int n, int 
         const double coef[3] = {PA_TANH_C0, PA_TANH_C1, PA_TANH_C2};
         mod.cap_in = (float)(2. * in * kLog2e);
         mod.cap_out = (float)to;
-        mod.range = (float)(PA_TANH_RANGE / in);
+        mod.range = (float)std::min(PA_TANH_RANGE / in, 0x1p60);       // the polynomial squares scores
         double f = to * in;
         for (int i = 0; i < 3; ++i, f *= in * in) {
             mod.c[i] = (float)(coef[i] * f);
@@ -65,7 +65,7 @@ int pa_prefill_scoremod(void *out, const void *q, const void *k_cache, const voi
 {
     if (workspace == nullptr || workspace_bytes < kPrefillWorkspaceBytes || !aligned16(workspace)) return PA_ERR_WORKSPACE;
     if (num_seqs < 0 || max_query_len < 0 || h_q <= 0 || h_kv <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 || window < 0 ||
-        h_q % h_kv != 0 || !std::isfinite(scale) || scale < 0x1p-64f || !valid_softcap(softcap) || cache_dtype < PA_CACHE_BF16 ||
+        h_q % h_kv != 0 || !(scale >= 0x1p-64f) || !valid_scores(scale, softcap) || cache_dtype < PA_CACHE_BF16 ||
         cache_dtype > PA_CACHE_INT8)
         return PA_ERR_INVALID_ARG;
     if (cache_dtype != PA_CACHE_BF16) return PA_ERR_UNSUPPORTED;

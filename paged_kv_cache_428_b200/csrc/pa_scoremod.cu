@@ -20,7 +20,7 @@ int pa_decode_scoremod(void *out, const void *q, const void *k_cache, const void
                        const float *alibi_slopes, int window, int cache_dtype, void *workspace, size_t workspace_bytes,
                        void *stream)
 {
-    if (cache_dtype < PA_CACHE_BF16 || cache_dtype > PA_CACHE_INT8 || !valid_softcap(softcap)) return PA_ERR_INVALID_ARG;
+    if (cache_dtype < PA_CACHE_BF16 || cache_dtype > PA_CACHE_INT8 || !valid_scores(scale, softcap)) return PA_ERR_INVALID_ARG;
     if (cache_dtype != PA_CACHE_BF16) return PA_ERR_UNSUPPORTED;
     const SplitCall c{out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, num_seqs, max_context_len,
                       h_q, h_kv, head_dim, block_size, num_blocks, scale, window, workspace, workspace_bytes, stream};

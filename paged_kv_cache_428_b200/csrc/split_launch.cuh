@@ -63,7 +63,7 @@ struct SplitCall {
 int split_prepare(SplitParams &p, const SplitCall &c, size_t more)
 {
     if (c.num_seqs < 0 || c.max_context_len < 0 || c.h_q <= 0 || c.h_kv <= 0 || c.num_blocks <= 0 ||
-        c.max_blocks_per_seq <= 0 || c.window < 0 || c.h_q % c.h_kv != 0 || !std::isfinite(c.scale))
+        c.max_blocks_per_seq <= 0 || c.window < 0 || c.h_q % c.h_kv != 0 || !std::isfinite(c.scale * kLog2e))
         return PA_ERR_INVALID_ARG;
     if (!supported_head_dim(c.head_dim) || !supported_block_size(c.block_size) || !supported_group(c.h_q / c.h_kv))
         return PA_ERR_UNSUPPORTED;

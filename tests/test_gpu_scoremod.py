@@ -168,6 +168,12 @@ def test_scores_that_are_all_zero(softcap):
     _prefill([60, 0], [80, 30], 2, 4, 16, 64, 24, softcap=softcap, q_factor=0.0)
 
 
+def test_prefill_scores_whose_squares_leave_fp32():
+    """Scores of 1e19 and more under a cap far above them."""
+    _prefill([60, 0], [80, 30], 2, 4, 16, 64, 25, softcap=1e25, q_factor=1e19)
+    _decode([200, 33], 2, 4, 16, 64, 25, softcap=1e25, q_factor=1e19)
+
+
 def test_decode_without_any_is_decode():
     gen = _gen(5)
     k, v, tab, _ = _pool([400, 77], 2, 16, 128, gen)

@@ -48,6 +48,15 @@ def test_prefill_refusals(kw, status):
     assert _prefill(**kw) == status
 
 
+@pytest.mark.parametrize("kw,status", [
+    (dict(cap=2.3e38), 0), (dict(cap=2.4e38), -1), (dict(cap=2.0 ** -64), 0), (dict(cap=2.0 ** -64, scale=1e19), -1),
+    (dict(cap=1.0, scale=1e19), 0), (dict(scale=2.4e38), -1), (dict(cap=0.5, scale=1e38), -1)])
+def test_scales_and_caps_that_leave_fp32(kw, status):
+    """What scores are multiplied by is finite: infinity times a score of 0 would be NaN."""
+    assert _decode(B=0, **kw) == status
+    assert _prefill(B=0, **kw) == status
+
+
 def test_workspace_goes_by_the_window():
     size = pa.pa_decode_scoremod_workspace_size
     assert size(1, 8, 2, 64, 100000, 100) < size(1, 8, 2, 64, 100000, 0)
