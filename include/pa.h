@@ -469,7 +469,8 @@ int pa_decode_weights(void *out, float *weights, int64_t weights_stride, const v
  *   new_weights    device fp32, rows of new_weights_stride >= budget as in pa_decode_weights: the kept
  *                  tokens' weights, then zeros up to the row's end (room for the tokens that follow)
  *   new_context_lens device int32 [num_seqs]: m
- *   max_context_len host-known bound of context_lens; sizes the launch (weights_stride >= it)
+ *   max_context_len host-known bound of context_lens; sizes the launch (weights_stride >= it).  Longer contexts,
+ *                  up to weights_stride, are evicted all the same, more slowly.
  *   cache_dtype    any; only rows of head_dim elements are moved.  (Rows of a block-scaled cache cannot
  *                  move between blocks.)
  * new_weights and new_context_lens must not overlap weights and context_lens (PA_ERR_INVALID_ARG).  A context

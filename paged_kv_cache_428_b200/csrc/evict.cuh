@@ -380,8 +380,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const Evict
 // ---- moving the rows ------------------------------------------------------------------------------
 constexpr int kMoveWarps = 8;
 
-// grid (ceil(budget / rows of a CTA), h_kv, B).  LPR: 16-byte chunks of one row.  A warp moves 32 / LPR rows of K
-// and of V at a time, four such steps in flight.  Bound by HBM: 268 MB in 44 us, 6.1 TB/s.
+// grid (CTAs for the rows that the host expects, at least one; h_kv, B).  LPR: 16-byte chunks of one row.  A warp moves
+// 32 / LPR rows of K and of V at a time, four such steps in flight, and goes on behind the grid's last row where more
+// stay (contexts above the host's bound).  Bound by HBM: 268 MB in 44 us, 6.1 TB/s.
 template <int LPR>
 __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const EvictParams p)
 {
@@ -389,41 +390,45 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const Evict
     const int kvh = blockIdx.y, seq = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const EvictCounts n(p, seq);
     pdl_wait();                                                // the choice is complete
-    const int j0 = (blockIdx.x * kMoveWarps + warp) * ROWS + lane / LPR;
-    const int col = lane % LPR;
-    if ((int)(blockIdx.x * kMoveWarps + warp) * ROWS >= n.size) return;
+    const int col = lane % LPR, shift = __ffs(p.block_size) - 1, low = p.block_size - 1;     // a power of two
     const int32_t *kept = p.kept + ((size_t)seq * p.h_kv + kvh) * p.budget;
     const int32_t *from = p.block_tables + (size_t)seq * p.max_blocks, *to = p.new_tables + (size_t)seq * p.new_max_blocks;
     const uint4 *k = reinterpret_cast<const uint4 *>(p.k_cache), *v = reinterpret_cast<const uint4 *>(p.v_cache);
-    int64_t src[U], dst[U];                                    // 16-byte chunks; -1: no row
+#pragma unroll 1
+    for (unsigned first = (blockIdx.x * kMoveWarps + warp) * ROWS; first < (unsigned)n.size;
+         first += gridDim.x * kMoveWarps * ROWS) {
+        const int j0 = (int)first + lane / LPR;
+        int64_t src[U], dst[U];                                // 16-byte chunks; -1: no row
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int j = j0 + u * RPW;
-        src[u] = dst[u] = -1;
-        if (j < n.size) {
-            const int t = kept[j], sb = t / p.block_size, db = j / p.block_size;
-            const int a = t >= 0 && sb < p.max_blocks ? __ldg(from + sb) : -1, b = db < p.new_max_blocks ? __ldg(to + db) : -1;
-            if (a >= 0 && a < p.num_blocks && b >= 0 && b < p.num_blocks) {
-                src[u] = (((int64_t)a * p.h_kv + kvh) * p.block_size + t % p.block_size) * LPR + col;
-                dst[u] = (((int64_t)b * p.h_kv + kvh) * p.block_size + j % p.block_size) * LPR + col;
-            } else if (col == 0) {
-                record_error(PA_DEVERR_BAD_BLOCK);
+        for (int u = 0; u < U; ++u) {
+            const int j = j0 + u * RPW;
+            src[u] = dst[u] = -1;
+            if (j < n.size) {
+                const int t = kept[j], sb = t >> shift, db = j >> shift;
+                const int a = t >= 0 && sb < p.max_blocks ? __ldg(from + sb) : -1;
+                const int b = db < p.new_max_blocks ? __ldg(to + db) : -1;
+                if (a >= 0 && a < p.num_blocks && b >= 0 && b < p.num_blocks) {
+                    src[u] = (((int64_t)a * p.h_kv + kvh) * p.block_size + (t & low)) * LPR + col;
+                    dst[u] = (((int64_t)b * p.h_kv + kvh) * p.block_size + (j & low)) * LPR + col;
+                } else if (col == 0) {
+                    record_error(PA_DEVERR_BAD_BLOCK);
+                }
             }
         }
+        uint4 a[U], b[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (src[u] >= 0) {
+                a[u] = __ldcs(k + src[u]);
+                b[u] = __ldcs(v + src[u]);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (src[u] >= 0) {
+                reinterpret_cast<uint4 *>(p.k_cache)[dst[u]] = a[u];
+                reinterpret_cast<uint4 *>(p.v_cache)[dst[u]] = b[u];
+            }
     }
-    uint4 a[U], b[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (src[u] >= 0) {
-            a[u] = __ldcs(k + src[u]);
-            b[u] = __ldcs(v + src[u]);
-        }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (src[u] >= 0) {
-            reinterpret_cast<uint4 *>(p.k_cache)[dst[u]] = a[u];
-            reinterpret_cast<uint4 *>(p.v_cache)[dst[u]] = b[u];
-        }
 }
 
 }  // namespace pa

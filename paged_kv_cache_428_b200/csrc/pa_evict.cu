@@ -48,7 +48,7 @@ template <int LPR>
 int launch_move(const EvictParams &p, int num_seqs, int most, cudaStream_t st)
 {
     const int rows = 32 / LPR * 4 * kMoveWarps;
-    return launch_ex(evict_move_kernel<LPR>, dim3((most + rows - 1) / rows, p.h_kv, num_seqs), dim3(kMoveWarps * 32), 0, st,
+    return launch_ex(evict_move_kernel<LPR>, dim3(std::max(1, (most + rows - 1) / rows), p.h_kv, num_seqs), dim3(kMoveWarps * 32), 0, st,
                      true, p);
 }
 
@@ -151,7 +151,7 @@ int pa_evict(void *k_cache, void *v_cache, const float *weights, int64_t weights
     p.recent = recent;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int rc = launch_select(p, num_seqs, max_context_len, st);
-    if (rc != PA_OK || most == 0) return rc;
+    if (rc != PA_OK) return rc;
     switch (head_dim * (cache_dtype == PA_CACHE_BF16 ? 2 : 1) / 16) {
     case 4: return launch_move<4>(p, num_seqs, most, st);
     case 8: return launch_move<8>(p, num_seqs, most, st);

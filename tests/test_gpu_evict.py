@@ -240,6 +240,12 @@ def test_evict_a_bound_below_the_contexts():
     _evict_case([20000, 9000], 1, 64, 64, 600, 100, 1, max_len=700)
 
 
+@pytest.mark.parametrize("max_len", [0, 1, 200, 599])
+def test_evict_a_bound_below_the_budget(max_len):
+    """The bound sizes the launch only: contexts that pass it, and the budget above it, keep all their rows."""
+    _evict_case([20000, 9000, 50, 0, 601], 2, 64, 64, 600, 100, 1, max_len=max_len)
+
+
 @pytest.mark.parametrize("what", ["zero", "one", "nan", "negative", "inf", "tiny", "two"])
 @pytest.mark.parametrize("n", [600, 30000])
 def test_evict_weights_that_are_alike(what, n):
