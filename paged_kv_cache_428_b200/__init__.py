@@ -23,6 +23,7 @@ Functions keep the C names:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from pathlib import Path
@@ -150,6 +151,19 @@ def _stream_ptr(stream) -> Optional[int]:
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def _owner(stream) -> contextlib.AbstractContextManager:
+    """What a call allocates for itself inside this context belongs to the stream it runs on: it is filled there,
+    and its memory goes to nobody else before the work queued there is done."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)
+        if handle == 2:                        # cudaStreamPerThread: no stream that torch could order its memory by
+            raise ValueError("a call on the per-thread default stream needs a workspace")
+        stream = torch.cuda.ExternalStream(handle) if handle > 2 else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _need(t: torch.Tensor, name: str, dtypes, ndim: Optional[int] = None, cuda: bool = True) -> None:
@@ -314,7 +328,8 @@ def pa_decode(out, q, k_cache, v_cache, block_tables, context_lens, max_context_
     Quantised caches take float scales (per tensor) or CUDA fp32 [h_kv] tensors (per KV head,
     pa_decode_head_scales)."""
     if workspace is None:
-        workspace = make_workspace(q.shape[0], q.shape[1], q.shape[2], max_context_len, partition_size, q.device)
+        with _owner(stream):
+            workspace = make_workspace(q.shape[0], q.shape[1], q.shape[2], max_context_len, partition_size, q.device)
     args = _decode_args(out, q, k_cache, v_cache, block_tables, context_lens, max_context_len, scale,
                         partition_size, k_scale, v_scale, workspace)
     heads = _head_scales(k_scale, v_scale, k_cache.shape[1])
@@ -366,7 +381,8 @@ def pa_decode_step(key, value, slot_mapping, out, q, k_cache, v_cache, block_tab
     """One decode step: write each sequence's appended token (row s of key/value, slot_mapping[s]),
     then attend; the decode overlaps the write (programmatic dependent launch).  Returns out."""
     if workspace is None:
-        workspace = make_workspace(q.shape[0], q.shape[1], q.shape[2], max_context_len, partition_size, q.device)
+        with _owner(stream):
+            workspace = make_workspace(q.shape[0], q.shape[1], q.shape[2], max_context_len, partition_size, q.device)
     args = step_call_args(key, value, slot_mapping, out, q, k_cache, v_cache, block_tables, context_lens,
                           max_context_len, scale, partition_size, k_scale, v_scale, workspace)
     _check(_lib.pa_decode_step(*args, _stream_ptr(stream)), "pa_decode_step")
@@ -556,9 +572,10 @@ def pa_decode_block_scales_workspace_size(num_seqs: int, h_q: int, h_kv: int, he
     return int(_lib.pa_decode_block_scales_workspace_size(num_seqs, h_q, h_kv, head_dim, max_context_len))
 
 
-def _new_workspace(size: int, q: torch.Tensor) -> torch.Tensor:
-    """A zero-filled workspace of `size` bytes where q is."""
-    return torch.zeros(max(size, 16), dtype=torch.uint8, device=q.device)
+def _new_workspace(size: int, q: torch.Tensor, stream) -> torch.Tensor:
+    """A zero-filled workspace of `size` bytes where q is, for a call on `stream`."""
+    with _owner(stream):
+        return torch.zeros(max(size, 16), dtype=torch.uint8, device=q.device)
 
 
 def _need_decode(out, q, k_cache, v_cache, block_tables, context_lens, dtypes) -> tuple:
@@ -596,7 +613,7 @@ def pa_decode_block_scales(out, q, k_cache, v_cache, k_scales, v_scales, block_t
     _need_scales(k_scales, v_scales, NB, h_kv)
     ws = workspace
     if ws is None:
-        ws = _new_workspace(pa_decode_block_scales_workspace_size(B, h_q, h_kv, d, max_context_len), q)
+        ws = _new_workspace(pa_decode_block_scales_workspace_size(B, h_q, h_kv, d, max_context_len), q, stream)
     _need(ws, "workspace", (torch.uint8,), 1)
     _check(_lib.pa_decode_block_scales(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
@@ -639,7 +656,7 @@ def pa_decode_scoremod(out, q, k_cache, v_cache, block_tables, context_lens, max
     window = _window(window)
     ws = workspace
     if ws is None:
-        ws = _new_workspace(pa_decode_scoremod_workspace_size(B, h_q, h_kv, d, max_context_len, window), q)
+        ws = _new_workspace(pa_decode_scoremod_workspace_size(B, h_q, h_kv, d, max_context_len, window), q, stream)
     _need(ws, "workspace", (torch.uint8,), 1)
     _check(_lib.pa_decode_scoremod(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
@@ -706,7 +723,7 @@ def pa_decode_weights(out, weights, q, k_cache, v_cache, block_tables, context_l
         raise ValueError("weights must be [%d, %d, n], got %s" % (B, h_kv, tuple(weights.shape)))
     ws = workspace
     if ws is None:
-        ws = _new_workspace(pa_decode_weights_workspace_size(B, h_q, h_kv, d, max_context_len), q)
+        ws = _new_workspace(pa_decode_weights_workspace_size(B, h_q, h_kv, d, max_context_len), q, stream)
     _need(ws, "workspace", (torch.uint8,), 1)
     _check(_lib.pa_decode_weights(
         out.data_ptr(), weights.data_ptr(), weights.shape[2], q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
