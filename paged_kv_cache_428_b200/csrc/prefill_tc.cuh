@@ -171,7 +171,7 @@ struct PrefillSched {
 
 // No modification: causal softmax of the scaled scores.
 struct PrefillPlain {
-    static constexpr bool kOn = false;
+    static constexpr bool kOn = false, kCap = false;
 };
 
 template <int D, int BS, int G, int NQ_ = 2, int KST_ = 4, int VST_ = 4>
@@ -198,8 +198,8 @@ struct PrefillTcConfig {
     static constexpr int OFF_V = OFF_K + KST * KV_TILE;
     static constexpr int OFF_BARS = OFF_V + VST * KV_TILE;
     // k, v full/empty; per tile: s full, s free, p full x2, o done x2, drain, q full; item ring
-    // full x2 / empty x2; the V tail copy; per tile: Q landed (TMA)
-    static constexpr int NBARS = 2 * KST + 2 * VST + NQ * 9 + 5;
+    // full x2 / empty x2; the V and the K edge copy; per tile: Q landed (TMA)
+    static constexpr int NBARS = 2 * KST + 2 * VST + NQ * 9 + 6;
     static constexpr int OFF_ITEMS = OFF_BARS + NBARS * 8;   // item ring: 2 x 8 ints
     static constexpr int OFF_MISC = OFF_ITEMS + 64;       // tensor-memory base, abort flag
     static constexpr int OFF_SEQ = OFF_MISC + 16;         // query_start, context_lens, claim order
@@ -243,8 +243,8 @@ __global__ void __launch_bounds__(PrefillTcConfig<D, BS, G, NQ_, KST_, VST_>::TH
     uint64_t *s_full = bars + 2 * KST + 2 * VST, *s_free = s_full + NQ, *p_full = s_free + NQ, *o_done = p_full + 2 * NQ;
     uint64_t *drain = o_done + 2 * NQ;                          // one per query tile
     uint64_t *q_full = drain + NQ;                              // one per query tile: Q copied
-    uint64_t *item_full = q_full + NQ, *item_empty = item_full + 2, *v_tail = item_empty + 2;
-    uint64_t *q_land = v_tail + 1;                               // one per query tile: its Q tile landed (TMA)
+    uint64_t *item_full = q_full + NQ, *item_empty = item_full + 2, *v_tail = item_empty + 2, *k_tail = v_tail + 1;
+    uint64_t *q_land = k_tail + 1;                               // one per query tile: its Q tile landed (TMA)
     volatile int *items = reinterpret_cast<volatile int *>(smem + C::OFF_ITEMS);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
@@ -279,6 +279,7 @@ __global__ void __launch_bounds__(PrefillTcConfig<D, BS, G, NQ_, KST_, VST_>::TH
             mbar_init(&item_empty[s], C::ITEM_READERS);
         }
         mbar_init(v_tail, 1);
+        mbar_init(k_tail, 1);
         for (int q = 0; q < NQ; ++q) mbar_init(&q_land[q], 1);
         *abort_flag = 0;
         mbar_init_fence();
@@ -515,24 +516,12 @@ __global__ void __launch_bounds__(PrefillTcConfig<D, BS, G, NQ_, KST_, VST_>::TH
                 }
                 // V tile holding rows past the context: the copy lands on v_tail, the rows past
                 // the context are zeroed, and only then is the tile marked full (likewise the rows before
-                // the window)
+                // the window; and those of a K tile where scores are capped, as all scores of a tile have a
+                // say in how tanh is computed)
                 const bool head = Mod::kOn && t == 0 && tok_lo > tile * BN;
-                const bool tail = is_v && ((tile + 1) * BN > ctx || head);
-                uint64_t *bar = tail ? v_tail : &full[st];
+                const bool tail = (is_v || Mod::kCap) && ((tile + 1) * BN > ctx || head);
+                uint64_t *landing = is_v ? v_tail : k_tail, *bar = tail ? landing : &full[st];
                 uint8_t *dst = smem + (is_v ? C::OFF_V : C::OFF_K) + st * C::KV_TILE;
-                if constexpr (Mod::kOn) {
-                    // K rows of blocks that are not copied: 0 and not what an earlier item left there, as all
-                    // scores of a tile have a say in how tanh is computed
-                    if (Mod::kCap && !is_v && (skip > 0 || nb < BPT)) {
-                        const int n8 = skip * BS * 8, m8 = (BN - nb * BS) * 8;
-                        for (int idx = lane; idx < C::HALVES * (n8 + m8); idx += 32) {
-                            const int h = idx / (n8 + m8), i = idx % (n8 + m8), i8 = i < n8 ? i : nb * BS * 8 + i - n8;
-                            *reinterpret_cast<uint4 *>(dst + h * C::KV_HALF + i8 * 16) = make_uint4(0u, 0u, 0u, 0u);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                }
                 if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)((nb - skip) * C::HALVES * BS * 128));
                 __syncwarp();
                 if (mine)
@@ -540,7 +529,7 @@ __global__ void __launch_bounds__(PrefillTcConfig<D, BS, G, NQ_, KST_, VST_>::TH
                 ++issued;
                 if (tail) {
                     // our own copy: wait for it whatever the abort flag says (bounded)
-                    const int landed = __shfl_sync(FULL, lane == 0 ? (int)mbar_wait_bounded(v_tail, ntail & 1) : 0, 0);
+                    const int landed = __shfl_sync(FULL, lane == 0 ? (int)mbar_wait_bounded(landing, ntail & 1) : 0, 0);
                     ++ntail;
                     if (landed) {
                         if (Mod::kOn && head) {

@@ -281,6 +281,35 @@ def test_prefill_does_not_depend_on_what_lies_in_masked_places():
         assert torch.equal(first, _prefill(*lens, 2, 4, 16, 128, 15, **kw))
 
 
+@pytest.mark.parametrize("bs", [16, 32, 64])
+@pytest.mark.parametrize("kw", [dict(window=50), dict(), dict(alibi=True, prefix=True, window=90)], ids=str)
+def test_prefill_bits_do_not_depend_on_free_slots(bs, kw):
+    """Whatever an earlier owner left in slots without a token, behind the contexts and before the window: NaN, small
+    or large numbers, the output's bits are the same."""
+    gen, d, h, g = _gen(26), 128, 2, 4
+    cached, chunk = [130, 77, 300, 0], [70, 130, 20, 33]
+    lens = [a + b for a, b in zip(cached, chunk)]
+    k, v, tab, full = _pool(lens, h, bs, d, gen, kw.get("window", 0), chunk)
+    start = torch.zeros(5, dtype=torch.int32)
+    start[1:] = torch.cumsum(torch.tensor(chunk), 0)
+    q = torch.randn((sum(chunk), h * g, d), generator=gen).to(torch.bfloat16)
+    slopes = _slopes(h * g).to(DEV) if "alibi" in kw else None
+    prefix = torch.tensor([140, 0, 310, 9], dtype=torch.int32, device=DEV) if "prefix" in kw else None
+    ctx = torch.tensor(lens, dtype=torch.int32)
+    outs = []
+    for fill in (None, 0.0, 1.0, 1e4, 1e30):
+        kf, vf = (x if fill is None else torch.where(torch.isnan(x), (fill * torch.randn(x.shape, generator=gen)).to(x.dtype), x)
+                  for x in (k, v))
+        out = torch.empty_like(q, device=DEV)
+        pa.pa_prefill_scoremod(out, q.to(DEV), kf.to(DEV), vf.to(DEV), tab.to(DEV), start.to(DEV), ctx.to(DEV), max(chunk),
+                               pa.make_prefill_workspace(), softcap=30.0, alibi_slopes=slopes, window=kw.get("window", 0),
+                               prefix_lens=prefix)
+        outs.append(out)
+    assert torch.isfinite(outs[0]).all() and pa.pa_device_errors() == 0
+    for out in outs[1:]:
+        assert torch.equal(outs[0], out)
+
+
 def test_prefill_more_sequences_than_the_claim_order_keeps():
     n = 1100
     _prefill([(i * 5) % 40 for i in range(n)], [(i * 3) % 4 for i in range(n)], 1, 1, 16, 64, 10, window=20, softcap=10.0)
