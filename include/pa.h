@@ -440,7 +440,7 @@ int pa_decode_block_scales(void *out, const void *q, const void *k_cache, const 
  *                  are set to zero when it starts.  Places at or past context_lens[s] are left alone, and so
  *                  are the rows of a sequence whose result is not finite (a block outside the pool).
  *   weights_stride >= max_context_len (else PA_ERR_INVALID_ARG)
- *   max_context_len host-known bound of context_lens.  A longer context is still attended as a whole, but
+ *   max_context_len host-known bound of context_lens, at most 2^30 (else PA_ERR_UNSUPPORTED).  A longer context is still attended as a whole, but
  *                  its weights past the bound are not counted; flags PA_DEVERR_BAD_LENGTH.
  *   cache_dtype    PA_CACHE_BF16 (other types: PA_ERR_UNSUPPORTED)
  *   workspace      as in pa_decode_block_scales, of pa_decode_weights_workspace_size(...) bytes (the
@@ -473,8 +473,9 @@ int pa_decode_weights(void *out, float *weights, int64_t weights_stride, const v
  *                  up to weights_stride, are evicted all the same, more slowly.
  *   cache_dtype    any; only rows of head_dim elements are moved.  (Rows of a block-scaled cache cannot
  *                  move between blocks.)
- * new_weights and new_context_lens must not overlap weights and context_lens (PA_ERR_INVALID_ARG).  A context
- * longer than weights_stride keeps nothing and flags PA_DEVERR_BAD_LENGTH; a row whose block is outside the
+ * new_weights and new_context_lens must not overlap weights and context_lens (PA_ERR_INVALID_ARG).
+ * max_context_len and budget are at most 2^30 (else PA_ERR_UNSUPPORTED).  A context longer than weights_stride,
+ * or than 2^30, keeps nothing and flags PA_DEVERR_BAD_LENGTH; a row whose block is outside the
  * pool is skipped and flags PA_DEVERR_BAD_BLOCK.  Tokens keep what positions were worked into their K;
  * calls that go by distance (windows, distance biases) see the new places. */
 int pa_evict(void *k_cache, void *v_cache, const float *weights, int64_t weights_stride, const int32_t *block_tables,

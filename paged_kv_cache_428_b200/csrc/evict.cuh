@@ -60,6 +60,7 @@ struct AddWeightsParams {
     int h_kv;
 };
 
+constexpr int kMaxWeights = 1 << 30;                   // of one row: places are counted in 32 bits, in steps
 constexpr int kAddThreads = 128, kAddPer = 4;          // threads, tokens of each
 
 // grid (ceil(max_tokens / (threads * per)), h_kv, B).  Bound by latency (length, denominators and logits, 28 MB mostly
@@ -130,19 +131,20 @@ struct EvictParams {
     float *new_weights;            // [B][h_kv][new_stride]
     int32_t *new_lens;             // [B]
     int64_t stride, new_stride;
+    int longest;                   // context that the rows of weights, and the counts here, have room for
     int max_blocks, new_max_blocks;
     int h_kv, block_size, num_blocks;
     int budget, recent;
 };
 
 // What becomes of a sequence of ctx tokens: `older` of them compete for `need` places, the `last` ones stay.
-// A context longer than its row of weights is refused as a whole.
+// A context longer than its row of weights (or than kMaxWeights) is refused as a whole.
 struct EvictCounts {
     int size, last, older, need;
     __device__ __forceinline__ EvictCounts(const EvictParams &p, int seq)
     {
         int ctx = max(0, __ldg(p.context_lens + seq));
-        if (ctx > p.stride) ctx = 0;
+        if (ctx > p.longest) ctx = 0;
         size = min(ctx, p.budget);
         last = min(size, p.recent);
         older = ctx - last;
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const Evict
     }
     if (kvh == 0 && rank == 0 && tid == 0) {
         p.new_lens[seq] = n.size;
-        if (__ldg(p.context_lens + seq) > p.stride) record_error(PA_DEVERR_BAD_LENGTH);
+        if (__ldg(p.context_lens + seq) > p.longest) record_error(PA_DEVERR_BAD_LENGTH);
     }
     // what needs no choice: the last ones, and the end of the rows
     const int all = rank * NT + tid, step = ranks * NT;

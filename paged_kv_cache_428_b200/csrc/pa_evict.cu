@@ -64,7 +64,7 @@ extern "C" {
 
 size_t pa_decode_weights_workspace_size(int num_seqs, int h_q, int h_kv, int head_dim, int max_context_len)
 {
-    if (!split_sizes_ok(num_seqs, h_q, h_kv, head_dim, max_context_len)) return 0;
+    if (!split_sizes_ok(num_seqs, h_q, h_kv, head_dim, max_context_len) || max_context_len > kMaxWeights) return 0;
     return split_layout(num_seqs, h_q, h_kv, head_dim, max_context_len).end + logit_bytes(num_seqs, h_q, max_context_len);
 }
 
@@ -74,7 +74,7 @@ int pa_decode_weights(void *out, float *weights, int64_t weights_stride, const v
                       float scale, int cache_dtype, void *workspace, size_t workspace_bytes, void *stream)
 {
     if (cache_dtype < PA_CACHE_BF16 || cache_dtype > PA_CACHE_INT8 || weights_stride < max_context_len) return PA_ERR_INVALID_ARG;
-    if (cache_dtype != PA_CACHE_BF16) return PA_ERR_UNSUPPORTED;
+    if (cache_dtype != PA_CACHE_BF16 || max_context_len > kMaxWeights) return PA_ERR_UNSUPPORTED;
     const SplitCall c{out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, num_seqs, max_context_len,
                       h_q, h_kv, head_dim, block_size, num_blocks, scale, 0, workspace, workspace_bytes, stream};
     SplitParams p{};
@@ -119,7 +119,7 @@ int pa_evict(void *k_cache, void *v_cache, const float *weights, int64_t weights
     if (weights_stride < max_context_len || new_weights_stride < budget ||
         (long long)new_max_blocks_per_seq * block_size < most)
         return PA_ERR_INVALID_ARG;
-    if (h_kv > 65535 || num_seqs > 65535) return PA_ERR_UNSUPPORTED;
+    if (h_kv > 65535 || num_seqs > 65535 || max_context_len > kMaxWeights || budget > kMaxWeights) return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PA_OK;
     if (!k_cache || !v_cache || !weights || !block_tables || !context_lens || !new_block_tables || !kept || !new_weights ||
         !new_context_lens)
@@ -141,6 +141,7 @@ int pa_evict(void *k_cache, void *v_cache, const float *weights, int64_t weights
     p.new_weights = new_weights;
     p.new_lens = new_context_lens;
     p.stride = weights_stride;
+    p.longest = (int)std::min<int64_t>(weights_stride, kMaxWeights);
     p.new_stride = new_weights_stride;
     p.max_blocks = max_blocks_per_seq;
     p.new_max_blocks = new_max_blocks_per_seq;

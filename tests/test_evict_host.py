@@ -51,6 +51,17 @@ def test_evict_refusals(kw, status):
     assert _evict(**kw) == status
 
 
+def test_sizes_near_the_end_of_32_bits():
+    """Places are counted in 32 bits, in steps: bounds above 2^30 are refused before anything is computed from them."""
+    big, more = 2 ** 31 - 1, 2 ** 30 + 1
+    assert pa.pa_decode_weights_workspace_size(1, 1, 1, 64, 2 ** 30) > 2 ** 32
+    assert pa.pa_decode_weights_workspace_size(1, 1, 1, 64, more) == 0
+    for n in (more, big - 3, big):
+        assert _decode(B=1, hq=1, hkv=1, mc=n, st=1 << 31, wsb=1 << 62) == -2
+        assert _evict(B=0, mc=n, st=1 << 31) == -2
+        assert _evict(B=0, budget=n, ns=1 << 31, nm=1 << 28) == -2
+
+
 def test_binding_refuses():
     c = torch.zeros((4, 2, 16, 64), dtype=torch.bfloat16)
     i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731

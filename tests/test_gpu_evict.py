@@ -321,6 +321,21 @@ def test_evict_bad_blocks_and_lengths():
         pa.pa_evict(kc, vc, new_w, tab.to(DEV), new_len, new_tab.to(DEV), 50, 50, 5, kept, new_w, new_len.clone())
 
 
+def test_evict_a_context_past_the_countable():
+    """A length near the end of 32 bits over a row of weights that has room for it keeps nothing and is reported."""
+    g = _gen(8)
+    k, v, tab, free = _pool([100], 4, 1, 16, 64, g)
+    w = torch.empty((1, 1, 2 ** 31), device=DEV)
+    kept = torch.zeros((1, 1, 20), dtype=torch.int32, device=DEV)
+    new_w, new_len = torch.ones((1, 1, 20), device=DEV), torch.ones(1, dtype=torch.int32, device=DEV)
+    pa.pa_device_errors(clear=True)
+    for n in (2 ** 30 + 1, 2 ** 31 - 1):
+        pa.pa_evict(k.to(DEV), v.to(DEV), w, tab.to(DEV), torch.tensor([n], dtype=torch.int32, device=DEV),
+                    torch.tensor([free[:2]], dtype=torch.int32, device=DEV), 100, 20, 5, kept, new_w, new_len)
+        assert pa.pa_device_errors() == pa.PA_DEVERR_BAD_LENGTH
+        assert new_len.tolist() == [0] and bool((kept == -1).all()) and not new_w.any()
+
+
 def test_a_chat_that_outgrows_its_budget():
     """Append, decode with weights, evict when the budget is exceeded, go on: the attention is over the kept
     rows, and two sequences that share blocks do not disturb each other."""
