@@ -107,33 +107,40 @@ __device__ __forceinline__ uint32_t requantise4(uint32_t w, float was, float now
 constexpr int kScaleWriteWarps = 4;
 constexpr int kScaleWriteMaxChunk = 64;
 
-__device__ __forceinline__ void team_sync(int team, int threads)
+// All warps of a team of TW (barriers by constant numbers: by a variable one, a CTA would hold all 16).
+template <int TW>
+__device__ __forceinline__ void team_sync(int team)
 {
-    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(threads) : "memory");
+    static_assert(kScaleWriteWarps / TW <= 2, "one barrier a team");
+    if (kScaleWriteWarps == TW || team == 0) asm volatile("bar.sync 1, %0;" ::"n"(TW * 32) : "memory");
+    else asm volatile("bar.sync 2, %0;" ::"n"(TW * 32) : "memory");
 }
 
 // A run is a maximal stretch of tokens next to each other whose slots lie in one block.  A CTA looks after
 // the runs that begin in its `chunk` tokens, for `heads` KV heads.  First it finds for each run which token owns
-// which row of the block (the later one, if two have the same slot); then teams of TW warps take one (run, head,
+// which row of the block (the later one, if two have the same slot); then teams of warps take one (run, head,
 // K or V) at a time: the rows into registers, maximum over them, the scale, older rows requantised if it
-// grew, the rows' codes.  With TW = BS / (rows of 8 loads of a warp) a whole block is in the registers of its team
-// and its rows are read once; with TW = 1 (few tokens) a longer run's rows are read twice.
+// grew, the rows' codes.  A team is one warp where none of the CTA's runs has more rows than its 8 loads bring, else as
+// many warps as bring a whole block: 4096 one-token runs of 8 heads of 128 into blocks of 64 take 42.8 us by single
+// warps and 138 to 218 by whole-block teams, and prompts of 32768 tokens 57.8 and 45.0.
 //   37k tokens of 8 heads of 128 into INT8 blocks of 64, 229 MB: 131 us with a warp an item, rows read twice and IEEE
 // divisions; 77 us with teams and the residual step; 57 us with 8 CTAs of 4 warps an SM, one head each (66 at 4
 // CTAs of 8 warps and 4 heads); 54.6 us with two values an instruction, against 35 us for the bytes.  Issue slots (70 %)
 // and the latency of the lookups bound it.  32 tokens of 32 heads: 4.0 us.
-template <int D, int BS, int QT, int TW>
+template <int D, int BS, int QT>
 __global__ void __launch_bounds__(kScaleWriteWarps * 32, 8) write_block_scales_kernel(const BlockScaleWriteParams p)
 {
     constexpr unsigned FULL = 0xffffffffu;
     constexpr int LPR = D / 8, RPI = 32 / LPR;         // lanes per bf16 row, rows of one load
-    constexpr int KEEP = 8, ROWS = TW * KEEP * RPI;    // loads kept in registers, rows of a team's loads
+    constexpr int KEEP = 8;                            // loads kept in registers
+    constexpr int WHOLE = cmax(1, BS / (KEEP * RPI));  // warps whose loads are a whole block
+    static_assert(WHOLE * KEEP * RPI >= BS && kScaleWriteWarps % WHOLE == 0, "teams");
     constexpr int WINDOW = kScaleWriteMaxChunk + BS;   // tokens whose borders are looked at
     constexpr int WORDS = (WINDOW + 31) / 32;
     __shared__ uint32_t border[WORDS + 1];             // bit i: token t0 + i does not continue the run of t0 + i - 1
     __shared__ int run_first[kScaleWriteMaxChunk], run_lo[kScaleWriteMaxChunk], run_hi[kScaleWriteMaxChunk];
     __shared__ bool run_plain[kScaleWriteMaxChunk];    // row lo + i belongs to the run's token i
-    __shared__ int num_runs;
+    __shared__ int num_runs, any_long;                 // any_long: a run has more rows than one warp's loads
     __shared__ int owner_of[kScaleWriteMaxChunk][BS];
     __shared__ uint32_t team_max[2][kScaleWriteWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -144,7 +151,7 @@ __global__ void __launch_bounds__(kScaleWriteWarps * 32, 8) write_block_scales_k
         const long long slot = __ldg(reinterpret_cast<const long long *>(p.slot_mapping) + t);
         return slot >= 0 && slot < p.num_slots ? slot / BS : -1;
     };
-    if (threadIdx.x == 0) num_runs = 0;
+    if (threadIdx.x == 0) num_runs = any_long = 0;
     __syncthreads();
     const int window = p.chunk + BS;
     for (int i = threadIdx.x; i < (window + 31) / 32 * 32; i += blockDim.x) {
@@ -194,76 +201,71 @@ __global__ void __launch_bounds__(kScaleWriteWarps * 32, 8) write_block_scales_k
             run_lo[run] = lo;
             run_hi[run] = hi;
             run_plain[run] = plain;
+            if (hi - lo >= KEEP * RPI) any_long = 1;
         }
     }
     __syncthreads();
 
-    const int team = warp / TW, member = warp % TW;
-    const int sub = lane / LPR, col = lane % LPR;
-    const int h0 = blockIdx.y * p.heads, nh = min(p.heads, p.h_kv - h0);
-    const int items = num_runs * nh * 2;
-    int parity = 0;
-    for (int item = team; item < items; item += kScaleWriteWarps / TW, parity ^= 1) {
-        const bool is_v = item & 1;
-        const int h = h0 + (item >> 1) % nh, run = (item >> 1) / nh;
-        const int lo = run_lo[run], hi = run_hi[run];
-        const int *owner = owner_of[run];
-        const long long blk = block_of(t0 + run_first[run]);
-        const __nv_bfloat16 *rows = (is_v ? p.value : p.key) + (size_t)h * D;
-        const int64_t stride = is_v ? p.value_stride : p.key_stride;
-        uint8_t *tile = (is_v ? p.v_cache : p.k_cache) + ((size_t)blk * p.h_kv + h) * BS * D;
-        float *scale = (is_v ? p.v_scales : p.k_scales) + (size_t)blk * p.h_kv + h;
-        const float was = lo > 0 ? *scale : 0.f;       // a block written from its first row on has no older rows
-        uint4 v[KEEP];
-        auto row_of = [&](int base, int k) { return base + (member * KEEP + k) * RPI + sub; };
-        const bool plain = run_plain[run];
-        const uint4 *at = reinterpret_cast<const uint4 *>(rows + (t0 + run_first[run]) * stride) + col;
-        const int64_t step = stride / 8;               // of `at`, a row
-        auto load = [&](int base) {
+    // a run's rows are in its team's registers, all at once: of one warp, or of as many as hold a whole block
+    auto work = [&](auto team_warps) {
+        constexpr int TW = decltype(team_warps)::value;
+        const int team = warp / TW, member = warp % TW;
+        const int sub = lane / LPR, col = lane % LPR;
+        const int h0 = blockIdx.y * p.heads, nh = min(p.heads, p.h_kv - h0);
+        const int items = num_runs * nh * 2;
+        int parity = 0;
+        for (int item = team; item < items; item += kScaleWriteWarps / TW, parity ^= 1) {
+            const bool is_v = item & 1;
+            const int h = h0 + (item >> 1) % nh, run = (item >> 1) / nh;
+            const int lo = run_lo[run], hi = run_hi[run];
+            const int *owner = owner_of[run];
+            const long long blk = block_of(t0 + run_first[run]);
+            const __nv_bfloat16 *rows = (is_v ? p.value : p.key) + (size_t)h * D;
+            const int64_t stride = is_v ? p.value_stride : p.key_stride;
+            uint8_t *tile = (is_v ? p.v_cache : p.k_cache) + ((size_t)blk * p.h_kv + h) * BS * D;
+            float *scale = (is_v ? p.v_scales : p.k_scales) + (size_t)blk * p.h_kv + h;
+            const float was = lo > 0 ? *scale : 0.f;       // a block written from its first row on has no older rows
+            uint4 v[KEEP];
+            const int row0 = lo + member * KEEP * RPI + sub;           // of v[0]; v[k] is row0 + k * RPI
+            const bool plain = run_plain[run];
             if (plain) {
-                const uint4 *from = at + (row_of(base, 0) - lo) * step;
+                const uint4 *from = reinterpret_cast<const uint4 *>(rows + (t0 + run_first[run] + row0 - lo) * stride) + col;
 #pragma unroll
-                for (int k = 0; k < KEEP; ++k, from += RPI * step)
-                    v[k] = row_of(base, k) <= hi ? __ldg(from) : make_uint4(0, 0, 0, 0);
+                for (int k = 0; k < KEEP; ++k, from += RPI * (stride / 8))
+                    v[k] = row0 + k * RPI <= hi ? __ldg(from) : make_uint4(0, 0, 0, 0);
             } else {
 #pragma unroll
                 for (int k = 0; k < KEEP; ++k) {
-                    const int row = row_of(base, k), t = row <= hi ? owner[row] : -1;
+                    const int row = row0 + k * RPI, t = row <= hi ? owner[row] : -1;
                     v[k] = t >= 0 ? __ldg(reinterpret_cast<const uint4 *>(rows + t * stride) + col) : make_uint4(0, 0, 0, 0);
                 }
             }
-        };
-        // maximum of |x|, two at a time; NaN stays in it
-        auto max2 = [](uint32_t a, uint32_t b) {
-            const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
-            return *reinterpret_cast<const uint32_t *>(&m);
-        };
-        uint32_t top = 0;
-        for (int base = lo; base <= hi; base += ROWS) {
-            load(base);
+            // maximum of |x|, two at a time; NaN stays in it
+            auto max2 = [](uint32_t a, uint32_t b) {
+                const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
+                return *reinterpret_cast<const uint32_t *>(&m);
+            };
+            uint32_t top = 0;
 #pragma unroll
             for (int k = 0; k < KEEP; ++k) {
                 top = max2(top, max2(v[k].x & 0x7fff7fffu, v[k].y & 0x7fff7fffu));
                 top = max2(top, max2(v[k].z & 0x7fff7fffu, v[k].w & 0x7fff7fffu));
             }
-        }
-        auto over_team = [&](uint32_t m, int slot) {   // the maximum over the team's threads
-            m = __reduce_max_sync(FULL, m);
-            if constexpr (TW > 1) {
-                if (lane == 0) team_max[slot][warp] = m;
-                team_sync(team, TW * 32);
+            auto over_team = [&](uint32_t m, int slot) {   // the maximum over the team's threads
+                m = __reduce_max_sync(FULL, m);
+                if constexpr (TW > 1) {
+                    if (lane == 0) team_max[slot][warp] = m;
+                    team_sync<TW>(team);
 #pragma unroll
-                for (int i = 0; i < TW; ++i) m = max(m, team_max[slot][team * TW + i]);
-            }
-            return m;
-        };
-        top = over_team(max(top & 0xffffu, top >> 16), parity);
-        const bool finite = top < 0x7f80u;
-        if (!finite) {                                 // infinities and NaN take no part: once more without them
-            if constexpr (TW > 1) team_sync(team, TW * 32);
-            uint32_t m = 0;
-            for (int base = lo; base <= hi; base += ROWS) {
-                load(base);
+                    for (int i = 0; i < TW; ++i) m = max(m, team_max[slot][team * TW + i]);
+                }
+                return m;
+            };
+            top = over_team(max(top & 0xffffu, top >> 16), parity);
+            const bool finite = top < 0x7f80u;
+            if (!finite) {                                 // infinities and NaN take no part: once more without them
+                if constexpr (TW > 1) team_sync<TW>(team);
+                uint32_t m = 0;
 #pragma unroll
                 for (int k = 0; k < KEEP; ++k) {
                     const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
@@ -273,45 +275,45 @@ __global__ void __launch_bounds__(kScaleWriteWarps * 32, 8) write_block_scales_k
                         m = a < 0x7f80u ? max(m, a) : m;
                     }
                 }
+                top = over_team(m, parity);
             }
-            top = over_team(m, parity);
-        }
-        const float now = fmaxf(was, block_scale_of<QT>(__uint_as_float(top << 16)));
-        __syncwarp();                                  // (the team's barrier) every lane has read the old scale
-        if (lo > 0 && now > was) {
-            // the scale grew: the rows before the first new one move to it (16 codes at a time)
-            for (int i = member * 32 + lane; i < lo * (D / 16); i += TW * 32) {
-                uint4 c = reinterpret_cast<uint4 *>(tile)[i];
-                c.x = requantise4<QT>(c.x, was, now);
-                c.y = requantise4<QT>(c.y, was, now);
-                c.z = requantise4<QT>(c.z, was, now);
-                c.w = requantise4<QT>(c.w, was, now);
-                reinterpret_cast<uint4 *>(tile)[i] = c;
-            }
-        }
-        if (member == 0 && lane == 0) *scale = now;
-        const bool fast = finite && now >= 0x1p-100f && now <= 0x1p100f;
-        const float r = __frcp_rn(now);
-        const bool kept = hi - lo < ROWS;              // the rows are still in registers
-        auto store = [&](int base, auto encode) {
-            uint8_t *to = tile + (size_t)row_of(base, 0) * D + 8 * col;
-#pragma unroll
-            for (int k = 0; k < KEEP; ++k) {
-                const int row = row_of(base, k);
-                if (row <= hi && (plain || owner[row] >= 0)) {
-                    const float2 a = bf16x2_to_float2(v[k].x), b = bf16x2_to_float2(v[k].y);
-                    const float2 c = bf16x2_to_float2(v[k].z), d = bf16x2_to_float2(v[k].w);
-                    *reinterpret_cast<uint2 *>(to + k * RPI * D) =
-                        make_uint2(encode(a.x, a.y, b.x, b.y), encode(c.x, c.y, d.x, d.y));
+            const float now = fmaxf(was, block_scale_of<QT>(__uint_as_float(top << 16)));
+            __syncwarp();                                  // (the team's barrier) every lane has read the old scale
+            if (lo > 0 && now > was) {
+                // the scale grew: the rows before the first new one move to it (16 codes at a time)
+                for (int i = member * 32 + lane; i < lo * (D / 16); i += TW * 32) {
+                    uint4 c = reinterpret_cast<uint4 *>(tile)[i];
+                    c.x = requantise4<QT>(c.x, was, now);
+                    c.y = requantise4<QT>(c.y, was, now);
+                    c.z = requantise4<QT>(c.z, was, now);
+                    c.w = requantise4<QT>(c.w, was, now);
+                    reinterpret_cast<uint4 *>(tile)[i] = c;
                 }
             }
-        };
-        for (int base = lo; base <= hi; base += ROWS) {
-            if (!kept) load(base);
-            if (fast) store(base, [&](float x, float y, float z, float w) { return encode4_fast<QT>(x, y, z, w, now, r); });
-            else store(base, [&](float x, float y, float z, float w) { return encode4<QT>(x, y, z, w, now); });
+            if (member == 0 && lane == 0) *scale = now;
+            const bool fast = finite && now >= 0x1p-100f && now <= 0x1p100f;
+            const float r = __frcp_rn(now);
+            uint8_t *to = tile + (size_t)row0 * D + 8 * col;
+            auto store = [&](auto encode) {
+#pragma unroll
+                for (int k = 0; k < KEEP; ++k) {
+                    const int row = row0 + k * RPI;
+                    if (row <= hi && (plain || owner[row] >= 0)) {
+                        const float2 a = bf16x2_to_float2(v[k].x), b = bf16x2_to_float2(v[k].y);
+                        const float2 c = bf16x2_to_float2(v[k].z), d = bf16x2_to_float2(v[k].w);
+                        *reinterpret_cast<uint2 *>(to + k * RPI * D) =
+                            make_uint2(encode(a.x, a.y, b.x, b.y), encode(c.x, c.y, d.x, d.y));
+                    }
+                }
+            };
+            if (fast) store([&](float x, float y, float z, float w) { return encode4_fast<QT>(x, y, z, w, now, r); });
+            else store([&](float x, float y, float z, float w) { return encode4<QT>(x, y, z, w, now); });
         }
+    };
+    if constexpr (WHOLE > 1) {
+        if (any_long) return work(std::integral_constant<int, WHOLE>{});
     }
+    work(std::integral_constant<int, 1>{});
 }
 
 // scales[dst][:] = scales[src][:] for every (src, dst) pair, layer, and K/V.

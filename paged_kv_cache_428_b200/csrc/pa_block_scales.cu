@@ -10,19 +10,11 @@ namespace {
 
 bool quantised(int cache_dtype) { return cache_dtype == PA_CACHE_E4M3 || cache_dtype == PA_CACHE_INT8; }
 
-template <int D, int BS, int TW>
-void launch_write_team(int cache_dtype, dim3 grid, const BlockScaleWriteParams &p, cudaStream_t st)
-{
-    if (cache_dtype == PA_CACHE_E4M3) write_block_scales_kernel<D, BS, 1, TW><<<grid, kScaleWriteWarps * 32, 0, st>>>(p);
-    else write_block_scales_kernel<D, BS, 2, TW><<<grid, kScaleWriteWarps * 32, 0, st>>>(p);
-}
-
 template <int D, int BS>
 void launch_write(int cache_dtype, dim3 grid, const BlockScaleWriteParams &p, cudaStream_t st)
 {
-    constexpr int WHOLE = cmax(1, BS * D / 8 / 32 / 8);        // warps whose 8 loads each are a whole block
-    if (p.chunk == kScaleWriteMaxChunk) launch_write_team<D, BS, WHOLE>(cache_dtype, grid, p, st);
-    else launch_write_team<D, BS, 1>(cache_dtype, grid, p, st);
+    if (cache_dtype == PA_CACHE_E4M3) write_block_scales_kernel<D, BS, 1><<<grid, kScaleWriteWarps * 32, 0, st>>>(p);
+    else write_block_scales_kernel<D, BS, 2><<<grid, kScaleWriteWarps * 32, 0, st>>>(p);
 }
 
 template <int D>
@@ -64,9 +56,14 @@ int pa_reshape_and_cache_block_scales(const void *key, const void *value, int64_
     p.num_tokens = num_tokens;
     p.h_kv = h_kv;
     p.num_slots = (long long)num_blocks * block_size;
-    // few tokens: as many CTAs as there is work for, each with about one (run, K or V) for a warp; many: whole
-    // runs for teams of warps
-    p.chunk = num_tokens <= 512 ? 2 : kScaleWriteMaxChunk;
+    // As many tokens a CTA as leave one CTA for each of the 8 places of an SM: a CTA takes its runs a few at a time, and
+    // finding them costs about as much as writing one.  One-token runs of 8 heads of 128 into blocks of 64, in chunks of
+    // 2, 8 and 64: 512 tokens 10, 11 and 51 us, 4096 tokens 56, 45 and 64; prompts of 4096 tokens 21, 13 and 11 us, of
+    // 32768 (4, 8 and 64) 85, 61 and 45.
+    const int sms = sm_count();
+    if (sms < 1) return PA_ERR_CUDA;
+    p.chunk = 2;
+    while (p.chunk < kScaleWriteMaxChunk && (long long)num_tokens * h_kv >= (long long)2 * p.chunk * 8 * sms) p.chunk *= 2;
     p.heads = 1;
     const dim3 grid((num_tokens + p.chunk - 1) / p.chunk, (h_kv + p.heads - 1) / p.heads);
     if (grid.y > 65535) return PA_ERR_UNSUPPORTED;

@@ -93,6 +93,57 @@ def test_write_many_tokens(kind):
     c.check()
 
 
+def _write_all_heads(rows, cache, scales, slots, kind):
+    """ref.write_block_scales with all heads of a block at once (each slot once, finite values)."""
+    bs = cache.shape[2]
+    blocks = {}
+    for t, s in enumerate(slots):
+        blocks.setdefault(s // bs, []).append((s % bs, t))
+    for b, pairs in blocks.items():
+        off, t = (torch.tensor(x) for x in zip(*pairs))
+        first = int(off.min())
+        want = rows[t].abs().amax((0, 2)) / ref.QMAX[kind]
+        unit = 2.0 ** (torch.floor(torch.log2(want)) - 7)
+        old = scales[b] if first else torch.zeros_like(want)
+        now = torch.maximum(old, torch.ceil(want / unit) * unit)
+        grew = (now > old)[:, None, None]
+        again = ref.encode(cache[b, :, :first] * (old / now)[:, None, None], 1.0, kind)
+        cache[b, :, :first] = torch.where(grew, again, cache[b, :, :first])
+        cache[b][:, off] = ref.encode(rows[t] / now[:, None], 1.0, kind).transpose(0, 1)
+        scales[b] = now
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("seqs,h,bs,d", [(600, 1, 16, 64), (600, 3, 64, 128), (600, 16, 16, 64),
+                                           (900, 12, 32, 128), (1100, 16, 64, 64), (4096, 19, 16, 64)])
+def test_write_many_short_runs(kind, seqs, h, bs, d):
+    """The append of a large batch, one token for most sequences and prompts of up to five blocks for some, in
+    between: every number of tokens that a CTA looks after, CTAs with long runs, with short ones and with both."""
+    g, nb = _gen(seqs), seqs + 300
+    c = Cache(nb, h, bs, d, kind)
+    order = torch.randperm(nb, generator=g).tolist()
+    fill = torch.randint(0, 100, (nb, h, bs, d), generator=g).to(torch.int8)
+    fill = fill if kind == "int8" else fill.float().to(torch.float8_e4m3fn)
+    for got, want in ((c.k, c.rk), (c.v, c.rv)):
+        got.copy_(fill)
+        want.copy_(fill.double())
+    scale = 2.0 ** torch.randint(-12, -4, (nb, h), generator=g).float()
+    for t in (c.ks, c.vs, c.rks, c.rvs):
+        t.copy_(scale)
+    slots, at = [], 0
+    for s in range(seqs):
+        n = int(torch.randint(2, 5 * bs, (1,), generator=g)) if s % 31 == 7 and s < 900 else 1
+        blocks = 1 if n == 1 else -(-n // bs)
+        tab, at = order[at:at + blocks], at + blocks
+        slots += _slots(tab, 0, n, bs) if n > 1 else [tab[0] * bs + int(torch.randint(0, bs, (1,), generator=g))]
+    key, value = _rows(len(slots), h, d, g), _rows(len(slots), h, d, g)
+    pa.pa_reshape_and_cache_block_scales(key.to(DEV), value.to(DEV), c.k, c.v, c.ks, c.vs, torch.tensor(slots, device=DEV))
+    _write_all_heads(key.double(), c.rk, c.rks, slots, kind)
+    _write_all_heads(value.double(), c.rv, c.rvs, slots, kind)
+    c.check()
+    assert pa.pa_device_errors() == 0
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_write_values_where_it_can_go_wrong(kind):
     g, h, d, bs = _gen(3), 2, 64, 16
