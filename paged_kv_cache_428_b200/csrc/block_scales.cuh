@@ -29,7 +29,6 @@ struct BlockScaleWriteParams {
     int h_kv;
     long long num_slots;
     int chunk;                     // tokens whose runs one CTA looks after, a power of two
-    int heads;                     // KV heads of one CTA
 };
 
 template <int QT>
@@ -117,16 +116,17 @@ __device__ __forceinline__ void team_sync(int team)
 }
 
 // A run is a maximal stretch of tokens next to each other whose slots lie in one block.  A CTA looks after
-// the runs that begin in its `chunk` tokens, for `heads` KV heads.  First it finds for each run which token owns
-// which row of the block (the later one, if two have the same slot); then teams of warps take one (run, head,
-// K or V) at a time: the rows into registers, maximum over them, the scale, older rows requantised if it
+// the runs that begin in its `chunk` tokens, for one KV head.  First it finds for each run which token owns
+// which row of the block (the later one, if two have the same slot); then teams of warps take one (run, K or V)
+// at a time: the rows into registers, maximum over them, the scale, older rows requantised if it
 // grew, the rows' codes.  A team is one warp where none of the CTA's runs has more rows than its 8 loads bring, else as
-// many warps as bring a whole block: 4096 one-token runs of 8 heads of 128 into blocks of 64 take 42.8 us by single
-// warps and 138 to 218 by whole-block teams, and prompts of 32768 tokens 57.8 and 45.0.
+// many warps as bring a whole block: 4096 one-token runs of 8 heads of 128 into blocks of 64 take 44 us by single
+// warps and 138 to 218 by whole-block teams, and prompts of 32768 tokens 58 and 44.
 //   37k tokens of 8 heads of 128 into INT8 blocks of 64, 229 MB: 131 us with a warp an item, rows read twice and IEEE
 // divisions; 77 us with teams and the residual step; 57 us with 8 CTAs of 4 warps an SM, one head each (66 at 4
-// CTAs of 8 warps and 4 heads); 54.6 us with two values an instruction, against 35 us for the bytes.  Issue slots (70 %)
-// and the latency of the lookups bound it.  32 tokens of 32 heads: 4.0 us.
+// CTAs of 8 warps and 4 heads); 54.6 us with two values an instruction; 50.7 us with rows that always stay in
+// registers, against 35 us for the bytes.  Issue slots (70 %) and the latency of the lookups weigh most.  32 tokens of
+// 32 heads: 4.1 us.
 template <int D, int BS, int QT>
 __global__ void __launch_bounds__(kScaleWriteWarps * 32, 8) write_block_scales_kernel(const BlockScaleWriteParams p)
 {
@@ -211,12 +211,13 @@ __global__ void __launch_bounds__(kScaleWriteWarps * 32, 8) write_block_scales_k
         constexpr int TW = decltype(team_warps)::value;
         const int team = warp / TW, member = warp % TW;
         const int sub = lane / LPR, col = lane % LPR;
-        const int h0 = blockIdx.y * p.heads, nh = min(p.heads, p.h_kv - h0);
-        const int items = num_runs * nh * 2;
+        const int items = num_runs * 2;
         int parity = 0;
         for (int item = team; item < items; item += kScaleWriteWarps / TW, parity ^= 1) {
             const bool is_v = item & 1;
-            const int h = h0 + (item >> 1) % nh, run = (item >> 1) / nh;
+            const int run = item >> 1;
+            int h = blockIdx.y;
+            asm volatile("" : "+r"(h));                // what follows from it is not kept over the loop: it would spill
             const int lo = run_lo[run], hi = run_hi[run];
             const int *owner = owner_of[run];
             const long long blk = block_of(t0 + run_first[run]);

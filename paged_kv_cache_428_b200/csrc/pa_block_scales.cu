@@ -64,8 +64,7 @@ int pa_reshape_and_cache_block_scales(const void *key, const void *value, int64_
     if (sms < 1) return PA_ERR_CUDA;
     p.chunk = 2;
     while (p.chunk < kScaleWriteMaxChunk && (long long)num_tokens * h_kv >= (long long)2 * p.chunk * 8 * sms) p.chunk *= 2;
-    p.heads = 1;
-    const dim3 grid((num_tokens + p.chunk - 1) / p.chunk, (h_kv + p.heads - 1) / p.heads);
+    const dim3 grid((num_tokens + p.chunk - 1) / p.chunk, h_kv);
     if (grid.y > 65535) return PA_ERR_UNSUPPORTED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (head_dim == 64) launch_write_block<64>(block_size, cache_dtype, grid, p, st);
