@@ -43,6 +43,7 @@ int pa_reshape_and_cache_block_scales(const void *key, const void *value, int64_
     if (num_tokens == 0) return PA_OK;
     if (!key || !value || !k_cache || !v_cache || !k_scales || !v_scales || !slot_mapping) return PA_ERR_INVALID_ARG;
     if (!aligned16(key) || !aligned16(value) || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_INVALID_ARG;
+    if (h_kv > 65535) return PA_ERR_UNSUPPORTED;
     BlockScaleWriteParams p{};
     p.key = static_cast<const __nv_bfloat16 *>(key);
     p.value = static_cast<const __nv_bfloat16 *>(value);
@@ -65,7 +66,6 @@ int pa_reshape_and_cache_block_scales(const void *key, const void *value, int64_
     p.chunk = 2;
     while (p.chunk < kScaleWriteMaxChunk && (long long)num_tokens * h_kv >= (long long)2 * p.chunk * 8 * sms) p.chunk *= 2;
     const dim3 grid((num_tokens + p.chunk - 1) / p.chunk, h_kv);
-    if (grid.y > 65535) return PA_ERR_UNSUPPORTED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (head_dim == 64) launch_write_block<64>(block_size, cache_dtype, grid, p, st);
     else launch_write_block<128>(block_size, cache_dtype, grid, p, st);
