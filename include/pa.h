@@ -340,17 +340,19 @@ int pa_validate_slots(const int64_t *slot_mapping, int num_tokens, int block_siz
  * step) and t that of the key, in this order:
  *   x = scale * q . k
  *   softcap > 0:    x = softcap * tanh(x / softcap)      (0 = no cap; else at least 2^-64)
- *   alibi_slopes:   x = x - alibi_slopes[h] * |p - t|    (device fp32 [h_q], finite; NULL = no bias)
+ *   alibi_slopes:   x = x - alibi_slopes[h] * |p - t|    (device fp32 [h_q]; times any distance, and that over
+ *                   scale, finite in fp32; NULL = no bias)
  *   window > 0:     only tokens t > p - window are seen, the query's own among them (0 = no window)
  *   prefix_lens:    tokens t < prefix_lens[s] are seen by every row of sequence s (inside its window),
  *                   also those behind it (device int32 [num_seqs], at most context_lens[s] count; NULL =
  *                   causal).  Prefill only: a decode step sees no token behind it.
  * scale, softcap and 2 scale / softcap, each times log2(e), are finite in fp32 (else PA_ERR_INVALID_ARG).
- * And out = softmax(x) . V over the tokens seen.  Documents that must not see each other are sequences of
+ * The result is out = softmax(x) . V over the tokens seen.  Documents that must not see each other are sequences of
  * their own here (a row of block_tables and a stretch of query_start each), which is what a document mask
  * says.
  * Blocks that lie before the window of every row of the call are not read: their table entries need not be
- * valid, so that a serving program can give them away.  bf16 caches (others: PA_ERR_UNSUPPORTED).
+ * valid, so that a serving program that keeps its own tables can give them away (pa_alloc_free_seq frees whole
+ * sequences only).  bf16 caches (others: PA_ERR_UNSUPPORTED).
  * Accuracy as pa_decode and pa_prefill; a capped score to 2^-19 of itself or 2^-20 of the cap.
  *
  * pa_decode_scoremod: arguments as pa_decode.  workspace as in pa_decode_block_scales, of
@@ -364,8 +366,8 @@ int pa_decode_scoremod(void *out, const void *q, const void *k_cache, const void
                        void *stream);
 
 /* pa_prefill_scoremod: arguments, workspace (pa_prefill_workspace_size bytes) and errors as pa_prefill_ws, and
- * scale is at least 2^-64 (else PA_ERR_INVALID_ARG).  Rows of one chunk are worked on in tiles: V of tokens that some rows of a tile see
- * and others do not must be finite (as in pa_prefill). */
+ * scale is at least 2^-64 (else PA_ERR_INVALID_ARG).  Rows of one chunk are worked on in tiles: V of tokens that
+ * some rows of a tile see and others do not must be finite (as in pa_prefill). */
 int pa_prefill_scoremod(void *out, const void *q, const void *k_cache, const void *v_cache, const int32_t *block_tables,
                         int max_blocks_per_seq, const int32_t *query_start, const int32_t *context_lens, int num_seqs,
                         int max_query_len, int h_q, int h_kv, int head_dim, int block_size, int num_blocks, float scale,

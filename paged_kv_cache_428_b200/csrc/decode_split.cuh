@@ -12,9 +12,11 @@
 // than it saves) and at least 1/62 of the longest sequence, so that at most kSplitMaxPieces CTAs share one
 // (sequence, KV head) group.  Where the CTAs suffice for it, no range crosses the border of a group: each
 // group is cut into ceil(blocks / u) even pieces, and no CTA ends two groups; with no sequence longer than
-// kSplitWholeTokens each group is one piece, as its merge would take longer than its blocks (16 heads over 300
-// tokens: 7.2 us whole, 9.7 in pieces of 128; 32 heads over 1001 tokens: 14.6 and 10.6).  The lengths are read on
-// the device; the host's bound on them only sizes the grid.
+// kSplitWholeTokens each group is one piece, as its merge would take longer than its blocks.  Whole and in pieces of
+// 128: 8 groups of 256 tokens of 128 dims in bf16 7.5 and 8.1 us, of 384 9.5 and 8.4, of 512 11.6 and 8.6; 256 such
+// groups 11.3 and 15.4, 14.1 and 18.8, 16.5 and 20.2; 8 groups of codes of 64 dims 7.1 and 8.3, 8.2 and 8.6, 9.6 and
+// 8.6; 32 groups of 1001 tokens in bf16 14.6 and 10.6.  The border stands between few groups and many.  The
+// lengths are read on the device; the host's bound on them only sizes the grid.
 //   A producer warp streams the blocks' K and V tiles by 2-D TMA through an mbarrier ring, without a
 // pause between groups: lane j looks up triple j of the next 32 (and its scales) while the present 32
 // are issued.  Consumer warps take blocks in turn (mma.sync m16n8k16, tokens or head dims on
@@ -25,7 +27,7 @@
 // for another, and the merge adds in the order of the CTAs: results do not depend on timing.
 //
 // Bound by the bytes of K and V: 64 sequences of 512..4096 tokens (613 MB) 100 to 104 us, 32 x 4096 tokens of 32 heads
-// in E4M3 (1076 MB) 176 to 188 us, 91 to 94 and 88 to 93 % of the copy rate.  Single short sequences are bound by
+// in E4M3 (1076 MB) 167 to 188 us, 91 to 94 and 88 to 98 % of the copy rate.  Single short sequences are bound by
 // latency: 5.8 us for 2 x 37..81 tokens, of which three dependent loads (length, table, tiles) are about 2.
 //
 // Masked places.  Scores of tokens outside [first, ctx) become -inf by select, V rows there are
