@@ -125,7 +125,7 @@ __device__ __forceinline__ void team_sync(int team)
 //   37k tokens of 8 heads of 128 into INT8 blocks of 64, 229 MB: 131 us with a warp an item, rows read twice and IEEE
 // divisions; 77 us with teams and the residual step; 57 us with 8 CTAs of 4 warps an SM, one head each (66 at 4
 // CTAs of 8 warps and 4 heads); 54.6 us with two values an instruction; 50.7 us with rows that always stay in
-// registers, against 35 us for the bytes.  Issue slots (70 %) and the latency of the lookups weigh most.  32 tokens of
+// registers, against 35 us for the bytes.  Issue slots (61 %) and the latency of the lookups weigh most.  32 tokens of
 // 32 heads: 4.1 us.
 template <int D, int BS, int QT>
 __global__ void __launch_bounds__(kScaleWriteWarps * 32, 8) write_block_scales_kernel(const BlockScaleWriteParams p)

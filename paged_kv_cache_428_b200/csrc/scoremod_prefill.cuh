@@ -84,6 +84,8 @@ struct PrefillScoreMod {
             for (int i = 0; i < 64; i += 2)
                 m4[(i >> 1) & 3] = max3f(m4[(i >> 1) & 3], fabsf(__uint_as_float(at(i))), fabsf(__uint_as_float(at(i + 1))));
             const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+            // (rows of K that are no token are 0 by now: the K warp sees to it.  Leaving their columns out here took 131 to
+            // 134 us for the chunk case, against 118)
             if (!__any_sync(0xffffffffu, top > range)) {
 #pragma unroll
                 for (int i = 0; i < 64; i += 2) {
